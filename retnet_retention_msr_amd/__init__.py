@@ -34,6 +34,17 @@ __all__ = [
     "chunkwise_backward",
     "chunkwise_backward_workspace_bytes",
     "RetentionError",
+    "Norm",
+    "gated_recurrence",
+    "gated_recurrence_backward",
+    "gated_recurrence_step",
+    "gated_recurrence_workspace_bytes",
+    "gated_norm",
+    "gated_norm_backward",
+    "gated_norm_backward_workspace_bytes",
+    "residual_norm",
+    "residual_norm_backward",
+    "residual_norm_backward_workspace_bytes",
 ]
 
 
@@ -79,6 +90,8 @@ def _gn_struct(gn: Optional[GroupNorm], H: int, dv: int, device, gate=None, like
         if gate is not None:
             raise ValueError("a gate needs the GroupNorm epilogue (gn)")
         return None, ()
+    if getattr(gn, "rms", False):
+        raise ValueError("the epilogue has no root-mean-square form: use gated_norm on the output")
     keep = []
     ptrs = []
     for t in (gn.weight, gn.bias):
@@ -468,3 +481,17 @@ def chunkwise_backward(q, k, v, grad_o, gamma: GammaLike, chunk: int, state_in=N
         raise RetentionError("retention_chunkwise_backward", rc)
     return gq, gk, gv, grad_state_in
 
+
+from .block import (  # noqa: E402  (block.py uses the helpers above)
+    Norm,
+    gated_norm,
+    gated_norm_backward,
+    gated_norm_backward_workspace_bytes,
+    gated_recurrence,
+    gated_recurrence_backward,
+    gated_recurrence_step,
+    gated_recurrence_workspace_bytes,
+    residual_norm,
+    residual_norm_backward,
+    residual_norm_backward_workspace_bytes,
+)

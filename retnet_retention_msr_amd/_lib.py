@@ -34,6 +34,20 @@ EXPORTED = (
     "retention_chunkwise_backward",
 )
 
+# Every symbol include/retention_block.h declares.
+BLOCK_EXPORTED = (
+    "retention_gated_recurrence_workspace_bytes",
+    "retention_gated_recurrence",
+    "retention_gated_recurrence_backward",
+    "retention_gated_recurrence_step",
+    "retention_gated_norm",
+    "retention_gated_norm_backward_workspace_bytes",
+    "retention_gated_norm_backward",
+    "retention_residual_norm",
+    "retention_residual_norm_backward_workspace_bytes",
+    "retention_residual_norm_backward",
+)
+
 
 # RETENTION_ABI_VERSION of include/retention.h that the structures here mirror.
 ABI_VERSION = 4
@@ -44,6 +58,20 @@ class GnStruct(ctypes.Structure):
 
     _fields_ = [("eps", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("gate", ctypes.c_void_p)]
+
+
+class View(ctypes.Structure):
+    """retention_view_t: a [B, H, N, d] tensor's address and its strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_n", ctypes.c_longlong)]
+
+
+class NormStruct(ctypes.Structure):
+    """retention_norm_t: eps, the form and the device weight and bias pointers."""
+
+    _fields_ = [("eps", ctypes.c_float), ("rms", ctypes.c_int), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -59,7 +87,7 @@ def load():
             f"{LIB_PATH} is missing: build it with `python -m retnet_retention_msr_amd.build` "
             "(there is no fallback path)"
         )
-    _lib = open_library(LIB_PATH)
+    _lib = declare_block(open_library(LIB_PATH))
     return _lib
 
 
@@ -101,6 +129,34 @@ def open_library(path):
         raise RuntimeError(
             f"{path} has ABI version {lib.retention_abi_version()}, this binding expects {ABI_VERSION}: rebuild it"
         )
+    return lib
+
+
+def declare_block(lib):
+    """Declares the argument and result types of include/retention_block.h's entry points on ``lib``."""
+    vp, i, f, size = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    view, norm = ctypes.POINTER(View), ctypes.POINTER(NormStruct)
+    workspace = [vp, size, vp]  # workspace, its bytes, stream
+    lib.retention_gated_recurrence_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.retention_gated_recurrence_workspace_bytes.restype = size
+    lib.retention_gated_recurrence.argtypes = [view] * 3 + [i] * 6 + [vp, vp, vp, i, i] + workspace
+    lib.retention_gated_recurrence.restype = i
+    lib.retention_gated_recurrence_backward.argtypes = [view] * 6 + [i] * 6 + [vp, vp, vp, vp, i, i] + workspace
+    lib.retention_gated_recurrence_backward.restype = i
+    lib.retention_gated_recurrence_step.argtypes = [view] * 3 + [i] * 5 + [vp, i, vp, vp]
+    lib.retention_gated_recurrence_step.restype = i
+    lib.retention_gated_norm.argtypes = [view] * 3 + [i] * 5 + [norm, vp]
+    lib.retention_gated_norm.restype = i
+    lib.retention_gated_norm_backward_workspace_bytes.argtypes = [i] * 6
+    lib.retention_gated_norm_backward_workspace_bytes.restype = size
+    lib.retention_gated_norm_backward.argtypes = [view] * 5 + [i] * 5 + [norm, vp, vp] + workspace
+    lib.retention_gated_norm_backward.restype = i
+    lib.retention_residual_norm.argtypes = [view] * 4 + [i] * 5 + [norm, vp, f, vp]
+    lib.retention_residual_norm.restype = i
+    lib.retention_residual_norm_backward_workspace_bytes.argtypes = [i] * 5
+    lib.retention_residual_norm_backward_workspace_bytes.restype = size
+    lib.retention_residual_norm_backward.argtypes = [view] * 6 + [i] * 5 + [norm, vp, f, vp, vp, vp] + workspace
+    lib.retention_residual_norm_backward.restype = i
     return lib
 
 

@@ -1,0 +1,589 @@
+"""GPU parity of the block operators (gated recurrence, gated norm, residual norm and their gradients) with the fp64 oracle.
+
+Tolerance of an element: half a step of the output's type relative to the value (bf16 2^-8, fp32 2^-24), plus the bound
+that the oracle's ``*_error`` functions derive for the operator's fp32 arithmetic, plus 2^-120 for what underflows.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import retnet_retention_msr_amd as ret
+from oracle import block_oracle as orc
+from oracle import retention_oracle as rorc
+from retnet_retention_msr_amd import synthetic
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+EPS = 1e-5
+
+
+def _announce(msg):
+    print(f"[case] {msg}", flush=True)
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(shape, seed, dtype=F32, std=1.0, mean=0.0):
+    return (torch.randn(*shape, generator=_gen(seed)) * std + mean).to(dtype)
+
+
+def _gate(shape, seed, dtype, form):
+    """Pre-activations around 2 or log decays with memories from a token to a few hundred; a few -inf (a = 0) and, in the
+    sigmoid form, +inf (a = 1)."""
+    g = _randn(shape, seed, F32, 2.0, 2.0) if form == "sigmoid" else -torch.exp(_randn(shape, seed, F32, 2.0, -3.0))
+    flat = g.view(-1)
+    flat[:: 97] = -float("inf")
+    if form == "sigmoid":
+        flat[5:: 131] = float("inf")
+    return g.to(dtype)
+
+
+def _check(got, ref, err, what):
+    half = torch.finfo(got.dtype).eps / 2
+    g, err = orc.f64(got), np.broadcast_to(err, ref.shape)
+    assert g.shape == ref.shape, (what, g.shape, ref.shape)
+    assert np.all(np.isfinite(g)), (what, "not finite")
+    if not g.size:
+        return
+    over = np.abs(g - ref) - (half * (np.abs(ref) + err) + err + 2.0 ** -120)
+    i = np.unravel_index(np.argmax(over), over.shape)
+    assert over[i] <= 0, f"{what} at {i}: {g[i]!r}, not {ref[i]!r} (allowed {err[i] + half * abs(ref[i]):.3e})"
+
+
+def _strided(t, seed):
+    """The same values as columns of a wider tensor, starting at an odd column."""
+    wide = torch.full((*t.shape[:-1], 2 * t.shape[-1] + 3), float("nan"), dtype=t.dtype, device=DEV)
+    view = wide[..., 3: 3 + t.shape[-1]]
+    view.copy_(t)
+    return view
+
+
+# ---------------------------------------------------------------------------
+# Gated recurrence
+
+# Lengths around the pieces that a sequence is cut into (waves of 16 to 64 tokens, workgroups of up to 512), widths
+# around the 64 channels of a workgroup and the vector widths.
+SHAPES = [
+    ((1, 1, 1), "sigmoid", BF16), ((1, 1, 1), "log", F32), ((3, 2, 8), "log", BF16), ((2, 31, 64), "sigmoid", BF16),
+    ((1, 32, 72), "log", F32), ((1, 33, 65), "sigmoid", F32), ((2, 63, 3), "log", BF16), ((1, 64, 64), "sigmoid", BF16),
+    ((2, 65, 40), "sigmoid", F32), ((1, 127, 96), "log", BF16), ((1, 255, 24), "sigmoid", BF16),
+    ((2, 256, 128), "log", F32), ((1, 257, 64), "log", BF16), ((1, 511, 33), "sigmoid", BF16),
+    ((1, 513, 16), "sigmoid", F32), ((3, 1000, 200), "sigmoid", BF16), ((1, 2049, 70), "log", BF16),
+    ((1, 5000, 64), "sigmoid", BF16), ((1, 4097, 8), "log", F32), ((2, 3, 77, 24), "sigmoid", BF16),
+    ((1, 16, 700, 64), "log", BF16), ((2, 5, 300, 7), "sigmoid", F32),
+]
+
+
+def _states(shape):
+    return (*shape[:-2], shape[-1])
+
+
+@pytest.mark.parametrize("shape, form, dtype", SHAPES)
+@pytest.mark.parametrize("strided", [False, True])
+def test_recurrence_matches_the_oracle(shape, form, dtype, strided):
+    _announce(f"recurrence {shape} {form} {dtype} strided={strided}")
+    x, g = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form)
+    s0 = _randn(_states(shape), 3) if strided else None
+    place = (lambda t: _strided(t, 0)) if strided else (lambda t: t.to(DEV))
+    h, s1 = ret.gated_recurrence(place(x), place(g), form, state_in=None if s0 is None else s0.to(DEV), state_out=True)
+    torch.cuda.synchronize()
+    ref, end = orc.recurrence(x, g, form, s0)
+    e, e_end = orc.recurrence_error(x, g, form, s0)
+    _check(h, ref, e, "h")
+    _check(s1, end, e_end, "state")
+
+
+@pytest.mark.parametrize("shape, form, dtype", SHAPES)
+@pytest.mark.parametrize("strided", [False, True])
+def test_recurrence_backward_matches_the_oracle(shape, form, dtype, strided):
+    _announce(f"recurrence backward {shape} {form} {dtype} strided={strided}")
+    x, g, dh = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form), _randn(shape, 4, dtype)
+    s0, ds = (_randn(_states(shape), 3), _randn(_states(shape), 5)) if strided else (None, None)
+    h = torch.from_numpy(orc.recurrence(x, g, form, s0)[0]).to(dtype)
+    place = (lambda t: _strided(t, 0)) if strided else (lambda t: t.to(DEV))
+    dev = [None if t is None else t.to(DEV) for t in (s0, ds)]
+    dx, dg, ds0 = ret.gated_recurrence_backward(place(dh), place(x), place(g), place(h), form, state_in=dev[0],
+                                                grad_state_out=dev[1], grad_state_in=True)
+    torch.cuda.synchronize()
+    refs = orc.recurrence_backward(dh, x, g, h, form, s0, ds)
+    errs = orc.recurrence_backward_error(dh, x, g, h, form, s0, ds)
+    for got, ref, e, what in zip((dx, dg, ds0), refs, errs, ("grad_x", "grad_gate", "grad_state_in")):
+        _check(got, ref, e, what)
+
+
+def test_the_gradients_are_those_of_differences_of_the_forward():
+    """In fp32, a step along a random direction changes the kernel's own outputs by what its gradients say."""
+    shape, form = (1, 300, 64), "sigmoid"
+    _announce("recurrence gradients against differences")
+    x, g, dh = (_randn(shape, s).to(DEV) for s in (11, 12, 13))
+    s0, ds = _randn((1, 64), 14).to(DEV), _randn((1, 64), 15).to(DEV)
+    dirs = [_randn(shape, 16).to(DEV), _randn(shape, 17).to(DEV), _randn((1, 64), 18).to(DEV)]
+    h, _ = ret.gated_recurrence(x, g, form, state_in=s0)
+    grads = ret.gated_recurrence_backward(dh, x, g, h, form, state_in=s0, grad_state_out=ds, grad_state_in=True)
+
+    def loss(k, eps):
+        at = [x, g, s0]
+        at[k] = at[k] + eps * dirs[k]
+        y, end = ret.gated_recurrence(at[0], at[1], form, state_in=at[2], state_out=True)
+        return ((y.double() * dh).sum() + (end.double() * ds).sum()).item()
+
+    # Central differences of step e err by O(e^2) of the third derivative and by the outputs' fp32 roundings over e:
+    # 2^-24 * sqrt(19200 terms) * a few / 2e = 3e-3 at e = 2^-8, against directional derivatives of order 100.
+    for k in range(3):
+        e = 2.0 ** -8
+        slope = (loss(k, e) - loss(k, -e)) / (2 * e)
+        want = (grads[k].double() * dirs[k]).sum().item()
+        assert abs(slope - want) <= 2e-2 + 1e-3 * abs(want), (k, slope, want)
+
+
+@pytest.mark.parametrize("dtype, form, d, heads", [(BF16, "sigmoid", 72, 0), (F32, "log", 33, 0), (BF16, "log", 64, 3)])
+def test_packed_sequences(dtype, form, d, heads):
+    """Ragged sequences, some empty, in one row with rows before, behind and (past max_len) between them that stay as
+    they were; against each sequence on its own."""
+    _announce(f"packed {dtype} {form} d={d} heads={heads}")
+    lens = [5, 0, 700, 1, 64, 0, 300, 2, 0]
+    cu = np.concatenate([[3], 3 + np.cumsum(lens)])
+    T, max_len = int(cu[-1]) + 9, 520  # the sequence of 700 is cut at 520
+    lead = (1, heads) if heads else (1,)
+    shape = (*lead, T, d)
+    x, g, dh = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form), _randn(shape, 3, dtype)
+    S = len(lens)
+    states = (S, heads, d) if heads else (S, d)
+    s0, ds = _randn(states, 4), _randn(states, 5)
+    mark = 7.5
+    out = torch.full(shape, mark, dtype=dtype, device=DEV)
+    grads = [torch.full(shape, mark, dtype=dtype, device=DEV) for _ in range(2)]
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    dev = [t.to(DEV) for t in (x, g, s0, dh, ds)]
+    _, s1 = ret.gated_recurrence(dev[0], dev[1], form, state_in=dev[2], state_out=True, cu_seqlens=cud, max_len=max_len, out=out)
+    _, _, ds0 = ret.gated_recurrence_backward(dev[3], dev[0], dev[1], out, form, state_in=dev[2], grad_state_out=dev[4],
+                                              grad_state_in=True, cu_seqlens=cud, max_len=max_len, grads=grads)
+    torch.cuda.synchronize()
+    left = torch.ones(T, dtype=torch.bool)
+    for i in range(S):
+        a, b = int(cu[i]), int(cu[i]) + min(lens[i], max_len)
+        left[a:b] = False
+        at = (0, Ellipsis, slice(a, b), slice(None))
+        args = (x[at], g[at], form, s0[i])
+        ref, end = orc.recurrence(*args)
+        e, e_end = orc.recurrence_error(*args)
+        _check(s1[i], end, e_end, f"state {i}")
+        h = out[at].cpu()
+        _check(h, ref, e, f"h {i}")
+        bargs = (dh[at], x[at], g[at], h, form, s0[i], ds[i])
+        for got, r, e, what in zip((grads[0][at], grads[1][at], ds0[i]), orc.recurrence_backward(*bargs),
+                                   orc.recurrence_backward_error(*bargs), ("grad_x", "grad_gate", "grad_state_in")):
+            _check(got, r, e, f"{what} {i}")
+    for t in (out, *grads):
+        assert bool((t.cpu()[..., left, :] == mark).all())
+
+
+def test_offsets_out_of_range_are_clamped():
+    _announce("offsets out of range")
+    T, d = 40, 16
+    x, g = _randn((1, T, d), 1).to(DEV), _gate((1, T, d), 2, F32, "log").to(DEV)
+    cu = torch.tensor([-5, 10, 25, 1000], dtype=torch.int32, device=DEV)
+    right = torch.tensor([0, 10, 25, 40], dtype=torch.int32, device=DEV)
+    h, s = ret.gated_recurrence(x, g, "log", state_out=True, cu_seqlens=cu)
+    h2, s2 = ret.gated_recurrence(x, g, "log", state_out=True, cu_seqlens=right)
+    assert torch.equal(h, h2) and torch.equal(s, s2)
+
+
+def test_states_in_place_and_fused_gradient_buffers():
+    """state_out may be state_in, grad_state_in grad_state_out, and the gradients two halves of one tensor."""
+    _announce("states in place")
+    shape, form = (2, 1500, 64), "sigmoid"
+    x, g, dh = _randn(shape, 1, BF16).to(DEV), _gate(shape, 2, BF16, form).to(DEV), _randn(shape, 3, BF16).to(DEV)
+    s0, ds = _randn((2, 64), 4).to(DEV), _randn((2, 64), 5).to(DEV)
+    h, s1 = ret.gated_recurrence(x, g, form, state_in=s0, state_out=True)
+    again = s0.clone()
+    h2, _ = ret.gated_recurrence(x, g, form, state_in=again, state_out=again)
+    assert torch.equal(h, h2) and torch.equal(again, s1)
+    dx, dg, ds0 = ret.gated_recurrence_backward(dh, x, g, h, form, state_in=s0, grad_state_out=ds, grad_state_in=True)
+    both, same = torch.empty(2, 1500, 128, dtype=BF16, device=DEV), ds.clone()
+    ret.gated_recurrence_backward(dh, x, g, h, form, state_in=s0, grad_state_out=same, grad_state_in=same,
+                                  grads=(both[..., :64], both[..., 64:]))
+    assert torch.equal(both[..., :64], dx) and torch.equal(both[..., 64:], dg) and torch.equal(same, ds0)
+
+
+def test_broadcast_gate():
+    """One gate for all rows of the batch (stride 0): the full gradient's sum over the rows is the gate's."""
+    _announce("broadcast gate")
+    shape = (3, 90, 64)
+    x, dh = _randn(shape, 1).to(DEV), _randn(shape, 2).to(DEV)
+    g1 = _gate((1, 90, 64), 3, F32, "sigmoid").to(DEV)
+    h, _ = ret.gated_recurrence(x, g1.expand(shape), "sigmoid")
+    want, _ = ret.gated_recurrence(x, g1.expand(shape).contiguous(), "sigmoid")
+    assert torch.equal(h, want)
+    _, dg, _ = ret.gated_recurrence_backward(dh, x, g1.expand(shape), h, "sigmoid")
+    _, ref, _ = ret.gated_recurrence_backward(dh, x, g1.expand(shape).contiguous(), h, "sigmoid")
+    assert dg.shape == shape and torch.equal(dg, ref)
+
+
+def test_log_form_needs_no_x():
+    _announce("log form without x")
+    shape = (1, 70, 40)
+    g, dh, h = _gate(shape, 1, BF16, "log").to(DEV), _randn(shape, 2, BF16).to(DEV), _randn(shape, 3, BF16).to(DEV)
+    a = ret.gated_recurrence_backward(dh, None, g, h, "log")
+    b = ret.gated_recurrence_backward(dh, h, g, h, "log")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("shape, dtype", [((1, 20000, 64), BF16), ((1, 16, 6000, 64), BF16), ((2, 3001, 200), F32)])
+def test_repeated_calls_are_bit_identical(shape, dtype):
+    _announce(f"repeated {shape} {dtype}")
+    x, g, dh = _randn(shape, 1, dtype).to(DEV), _gate(shape, 2, dtype, "sigmoid").to(DEV), _randn(shape, 3, dtype).to(DEV)
+    first = None
+    for _ in range(30):
+        h, s = ret.gated_recurrence(x, g, state_out=True)
+        dx, dg, ds = ret.gated_recurrence_backward(dh, x, g, h, grad_state_in=True)
+        got = [t.clone() for t in (h, s, dx, dg, ds)]
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_two_streams_at_once():
+    """Two calls that overlap on two streams, each with its own workspace and tensors, give what each gives alone."""
+    _announce("two streams")
+    shapes = [(1, 30000, 256), (2, 9000, 320)]
+    args = [(_randn(s, 1, BF16).to(DEV), _gate(s, 2, BF16, "sigmoid").to(DEV)) for s in shapes]
+    want = [ret.gated_recurrence(*a, state_out=True) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(5):
+        got = []
+        for st, a in zip(streams, args):
+            with torch.cuda.stream(st):
+                got.append(ret.gated_recurrence(*a, state_out=True))
+        torch.cuda.synchronize()
+        for (h, s), (h0, s0) in zip(got, want):
+            assert torch.equal(h, h0) and torch.equal(s, s0)
+
+
+# ---------------------------------------------------------------------------
+# One token
+
+@pytest.mark.parametrize("B, lead, d, dtype, form", [
+    (1, (), 1, F32, "sigmoid"), (1, (), 64, BF16, "log"), (5, (), 333, BF16, "sigmoid"), (8, (4,), 72, F32, "log"),
+    (300, (2,), 40, BF16, "sigmoid"), (3, (), 4096, BF16, "log"), (7, (), 2048, F32, "sigmoid")])
+@pytest.mark.parametrize("strided", [False, True])
+def test_step_matches_the_oracle(B, lead, d, dtype, form, strided):
+    _announce(f"step {B} {lead} {d} {dtype} {form} strided={strided}")
+    shape = (B, *lead, d)
+    x, g, s0 = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form), _randn(shape, 3)
+    place = (lambda t: _strided(t, 0)) if strided else (lambda t: t.to(DEV))
+    state = s0.to(DEV)
+    h = ret.gated_recurrence_step(place(x), place(g), state, form)
+    torch.cuda.synchronize()
+    tok = [t.unsqueeze(-2) for t in (x, g)]
+    ref, end = orc.recurrence(*tok, form, s0)
+    e, _ = orc.recurrence_error(*tok, form, s0)
+    _check(h, ref[..., 0, :], e[..., 0, :], "h")
+    _check(state, end, e[..., 0, :], "state")
+
+
+@pytest.mark.parametrize("dtype, d", [(BF16, 96), (F32, 35)])
+def test_step_with_slots(dtype, d):
+    """Rows pick states of a pool; idle rows (slots below 0 or beyond the pool) and unnamed states stay as they were; rows
+    of one slot take effect in row order."""
+    _announce(f"slots {dtype} {d}")
+    P, slots = 12, [3, -1, 7, 3, 11, 12, 0, 3, 7, -2147483648, 2147483647]
+    B = len(slots)
+    x, g, pool = _randn((B, d), 1, dtype), _gate((B, d), 2, dtype, "sigmoid"), _randn((P, d), 3)
+    out = torch.full((B, d), 9.0, dtype=dtype, device=DEV)
+    state = pool.to(DEV)
+    ret.gated_recurrence_step(x.to(DEV), g.to(DEV), state, "sigmoid", slots=torch.tensor(slots, dtype=torch.int32, device=DEV), out=out)
+    torch.cuda.synchronize()
+    for s in range(P):
+        rows = [i for i, v in enumerate(slots) if v == s]
+        if not rows:
+            assert torch.equal(state[s].cpu(), pool[s])
+            continue
+        ref, end = orc.recurrence(x[rows], g[rows], "sigmoid", pool[s])
+        e, e_end = orc.recurrence_error(x[rows], g[rows], "sigmoid", pool[s])
+        _check(out[rows], ref, e, f"h of slot {s}")
+        _check(state[s], end, e_end, f"state {s}")
+    idle = [i for i, v in enumerate(slots) if not 0 <= v < P]
+    assert bool((out[idle] == 9.0).all())
+
+
+def test_prefill_then_steps_is_the_whole_sequence():
+    _announce("prefill and steps")
+    B, N, D, k = 2, 400, 128, 5
+    x, g = _randn((B, N, D), 1, BF16), _gate((B, N, D), 2, BF16, "sigmoid")
+    xd, gd = x.to(DEV), g.to(DEV)
+    _, state = ret.gated_recurrence(xd[:, :N - k], gd[:, :N - k], state_out=True)
+    h = [ret.gated_recurrence_step(xd[:, t], gd[:, t], state) for t in range(N - k, N)]
+    torch.cuda.synchronize()
+    ref, end = orc.recurrence(x, g, "sigmoid")
+    e, e_end = orc.recurrence_error(x, g, "sigmoid")
+    _check(torch.stack(h, 1), ref[:, N - k:], e[:, N - k:], "h")
+    _check(state, end, e_end, "state")
+
+
+# ---------------------------------------------------------------------------
+# Norms
+
+HEADS = [
+    (1, 1, 1, 1, BF16), (1, 2, 3, 8, F32), (2, 3, 5, 64, BF16), (1, 4, 7, 65, F32), (2, 2, 33, 96, BF16),
+    (1, 3, 50, 127, BF16), (3, 5, 21, 97, F32), (2, 8, 40, 256, BF16), (1, 4, 60, 320, F32), (2, 4, 130, 512, BF16),
+    (1, 2, 30, 513, BF16), (2, 3, 17, 1024, BF16), (1, 2, 9, 1024, F32), (1, 2, 11, 1023, F32), (4, 16, 1, 512, BF16),
+]
+
+
+def _norm_params(n, seed, which):
+    w = _randn((n,), seed, F32, 0.25, 1.0) if "w" in which else None
+    b = _randn((n,), seed + 1, F32, 0.1) if "b" in which else None
+    return w, b, dict(weight=None if w is None else w.to(DEV), bias=None if b is None else b.to(DEV))
+
+
+@pytest.mark.parametrize("B, H, N, d, dtype", HEADS)
+@pytest.mark.parametrize("rms, gated, which, strided", [(False, True, "wb", False), (True, True, "w", True),
+                                                         (False, False, "", True), (True, False, "b", False)])
+def test_gated_norm_matches_the_oracle(B, H, N, d, dtype, rms, gated, which, strided):
+    _announce(f"gated norm {B, H, N, d} {dtype} rms={rms} gate={gated} {which} strided={strided}")
+    shape = (B, H, N, d)
+    o, dy = _randn(shape, 1, dtype, 2.0, 0.5), _randn(shape, 2, dtype)
+    gate = _randn(shape, 3, dtype, 3.0) if gated else None
+    w, b, params = _norm_params(H * d, 4, which)
+    norm = ret.Norm(EPS, rms=rms, **params)
+    place = (lambda t: None if t is None else _strided(t, 0)) if strided else (lambda t: None if t is None else t.to(DEV))
+    od, gd = place(o), place(gate)
+    y = ret.gated_norm(od, gd, norm)
+    got = ret.gated_norm_backward(place(dy), od, gd, norm)
+    torch.cuda.synchronize()
+    args = (o, gate, w, b, EPS, rms)
+    _check(y, orc.gated_norm(*args), orc.gated_norm_error(*args), "y")
+    refs, errs = orc.gated_norm_backward(dy, *args), orc.gated_norm_backward_error(dy, *args)
+    for t, ref, e, what, wanted in zip(got, refs, errs, ("grad_o", "grad_gate", "grad_weight", "grad_bias"),
+                                       (True, gated, "w" in which, "b" in which)):
+        assert (t is not None) == wanted, what
+        if wanted:
+            _check(t, ref, e, what)
+
+
+def test_gated_norm_is_the_chunkwise_epilogue():
+    """On one token's and a sequence's worth of the retention's raw output, token-major output included."""
+    _announce("gated norm as the epilogue")
+    B, H, N, dk, dv, C = 2, 4, 200, 64, 128, 64
+    q, k, v = (t.to(DEV) for t in synthetic.make_qkv(B, H, N, dk, dv, dtype=F32, seed=3))
+    g = synthetic.head_gammas(H)
+    w, b = (t.to(DEV) for t in synthetic.make_gn_affine(H, dv, seed=4))
+    gate = synthetic.make_gate((B, H, N, dv), F32, seed=5).to(DEV)
+    gn = ret.GroupNorm(EPS, w, b)
+    raw, _ = ret.chunkwise(q, k, v, g, C)
+    fused, _ = ret.chunkwise(q, k, v, g, C, gn=gn, gate=gate)
+    y = ret.gated_norm(raw, gate, gn)
+    # Both norm the same fp32 values; each is within the operator's bound of the exact result.
+    args = (raw, gate, w, b, EPS, False)
+    _check(fused, orc.gated_norm(*args), orc.gated_norm_error(*args), "epilogue")
+    _check(y, orc.gated_norm(*args), orc.gated_norm_error(*args), "operator")
+    token_major = torch.empty(B, N, H, dv, device=DEV)
+    ret.gated_norm(raw, gate, gn, out=token_major.transpose(1, 2))
+    assert torch.equal(token_major.transpose(1, 2), y)
+    one = ret.gated_norm(raw[:, :, 7], gate[:, :, 7], gn)
+    assert torch.equal(one, y[:, :, 7])
+
+
+def test_msr_training_step():
+    """The gated MSR block's gradient chain: gated_norm_backward, then chunkwise_backward on what it gives, against the
+    oracle's."""
+    _announce("norm backward into retention backward")
+    B, H, N, dk, dv, C = 1, 3, 150, 32, 64, 64
+    q, k, v = synthetic.make_qkv(B, H, N, dk, dv, dtype=F32, seed=6)
+    g = synthetic.head_gammas(H)
+    gate, dy = synthetic.make_gate((B, H, N, dv), F32, seed=7), _randn((B, H, N, dv), 8)
+    w, b = synthetic.make_gn_affine(H, dv, seed=9)
+    dev = [t.to(DEV) for t in (q, k, v, gate, dy, w, b)]
+    gn = ret.GroupNorm(EPS, dev[5], dev[6])
+    o, _ = ret.chunkwise(*dev[:3], g, C)
+    do, dgate, dw, db = ret.gated_norm_backward(dev[4], o, dev[3], gn)
+    grads = ret.chunkwise_backward(*dev[:3], do, g, C)[:3]
+    torch.cuda.synchronize()
+    o_ref, _ = rorc.chunkwise(q, k, v, g, C)
+    refs = orc.gated_norm_backward(dy, o_ref, gate, w, b, EPS, False)
+    back = rorc.backward(q, k, v, g, refs[0])[:3]
+    # fp32 chunkwise results are held to 1e-4 of the head's largest value; the norm multiplies the relative error of
+    # its input by at most a few tens (values up to about five deviations, squared).
+    for got, ref in zip((do, dgate, dw, db, *grads), (*refs, *back)):
+        np.testing.assert_allclose(orc.f64(got), ref, rtol=0, atol=2e-3 * np.abs(ref).max())
+
+
+ROWS = [
+    ((1, 1), BF16, BF16), ((3, 8), F32, F32), ((5, 65), BF16, F32), ((2, 7, 64), BF16, BF16), ((2, 3, 5, 96), F32, F32),
+    ((130, 1000), BF16, F32), ((33, 1023), BF16, BF16), ((9, 1024), F32, F32), ((40, 2048), BF16, F32),
+    ((7, 2049), F32, F32), ((70, 4096), BF16, BF16), ((3, 5000), BF16, F32), ((5, 8192), F32, F32), ((4, 8192), BF16, F32),
+    ((3, 16384), BF16, BF16), ((2, 16384), F32, F32), ((2, 16383), BF16, F32), ((4096,), BF16, BF16),
+]
+
+
+@pytest.mark.parametrize("shape, dtype, stream", ROWS)
+@pytest.mark.parametrize("rms, scaled, alpha, which, strided", [(False, True, 1.75, "wb", False), (True, False, 1.0, "w", True),
+                                                                (True, True, 1.0, "", False), (False, False, 0.5, "b", True)])
+def test_residual_norm_matches_the_oracle(shape, dtype, stream, rms, scaled, alpha, which, strided):
+    _announce(f"residual norm {shape} {dtype} {stream} rms={rms} scale={scaled} alpha={alpha} {which} strided={strided}")
+    D = shape[-1]
+    x, res = _randn(shape, 1, dtype), _randn(shape, 2, stream, 2.0, 0.5)
+    dy, dr = _randn(shape, 3, dtype), _randn(shape, 4, stream)
+    scale = _randn((D,), 5, F32, 0.2, 0.7) if scaled else None
+    w, b, params = _norm_params(D, 6, which)
+    norm = ret.Norm(EPS, rms=rms, **params)
+    place = (lambda t: _strided(t, 0)) if strided and len(shape) in (2, 3) else (lambda t: t.to(DEV))
+    xd, sd = place(x), None if scale is None else scale.to(DEV)
+    y, r = ret.residual_norm(xd, place(res), norm, scale=sd, alpha=alpha)
+    with_dr = alpha != 0.5  # one of the four takes no gradient from the stream
+    got = ret.residual_norm_backward(place(dy), r, norm, grad_r=place(dr) if with_dr else None, x=xd, scale=sd, alpha=alpha)
+    torch.cuda.synchronize()
+    args = (x, res, w, b, EPS, rms, scale, alpha)
+    y_ref, r_ref = orc.residual_norm(*args)
+    e_y, e_r = orc.residual_norm_error(*args)
+    _check(y, y_ref, e_y, "y")
+    _check(r, r_ref, e_r, "r")
+    bargs = (dy, dr if with_dr else None, r.cpu(), w, EPS, rms, x, scale, alpha)
+    refs, errs = orc.residual_norm_backward(*bargs), orc.residual_norm_backward_error(*bargs)
+    for t, ref, e, what, wanted in zip(got, refs, errs, ("grad_x", "grad_residual", "grad_scale", "grad_weight", "grad_bias"),
+                                       (True, True, scaled, "w" in which, "b" in which)):
+        assert (t is not None) == wanted, what
+        if wanted:
+            _check(t, ref, e, what)
+    shared = not scaled and alpha == 1.0 and dtype == stream
+    assert (got[0] is got[1]) == shared
+
+
+def test_constant_rows_and_huge_values():
+    """A row of one value has no deviation: the layer form gives the bias. Values near the top of bf16's exponents that
+    still square in fp32, and rows of zeros in the rms form, stay finite."""
+    _announce("constant rows")
+    x = torch.full((2, 3, 4, 64), 3.0, dtype=BF16, device=DEV)
+    b = _randn((192,), 1).to(DEV)
+    y = ret.gated_norm(x, None, ret.Norm(EPS, None, b))
+    assert torch.equal(y, b.view(3, 1, 64).expand(2, 3, 4, 64).to(BF16))
+    assert bool((ret.gated_norm(torch.zeros_like(x), None, ret.Norm(EPS, rms=True)) == 0).all())
+    big = torch.full((1, 1, 1, 64), 1e17, dtype=BF16, device=DEV)
+    assert bool((ret.gated_norm(big, None, ret.Norm(EPS, rms=True)) == 1).all())
+    gate = torch.tensor([-1e4, 1e4] * 32, dtype=BF16, device=DEV).view(1, 1, 1, 64)
+    dy = torch.ones_like(big)
+    y = ret.gated_norm(big, gate, ret.Norm(EPS, rms=True)).view(-1)
+    assert bool((y[::2] == 0).all()) and bool((y[1::2] == gate.view(-1)[1]).all())
+    dgate = ret.gated_norm_backward(dy, big, gate, ret.Norm(EPS, rms=True))[1].view(-1)
+    assert bool((dgate[::2] == 0).all()) and bool((dgate[1::2] == 1).all())
+
+
+# ---------------------------------------------------------------------------
+# Together
+
+
+def _torch_block(x, res, gate, wg, scale, w1, w2, b2, form):
+    """The block in float64: residual and norm, gated recurrence, norm and gate, residual and norm."""
+    def norm(v, rms):
+        d = v if rms else v - v.mean(-1, keepdim=True)
+        return d / torch.sqrt((d * d).mean(-1, keepdim=True) + EPS)
+
+    B, N, D = x.shape
+    r1 = res + x
+    y1 = norm(r1, True) * w1
+    a = torch.sigmoid(gate)
+    now, hs = torch.zeros(B, D, dtype=torch.float64), []
+    for t in range(N):
+        now = a[:, t] * now + (1 - a[:, t]) * y1[:, t]
+        hs.append(now)
+    h = torch.stack(hs, 1)
+    H = 4
+    m = norm(h.view(B, N, H, D // H), False).view(B, N, D) * w2 + b2
+    m = m * torch.nn.functional.silu(wg)
+    r2 = r1 + scale * m
+    return norm(r2, True) * w1, r2
+
+
+def test_a_block_forward_and_backward():
+    """residual_norm, gated_recurrence, gated_norm, residual_norm in fp32 and back, against torch autograd in float64.
+    Every operator is within 1e-5 of its largest value (the per-operator bounds above); four of them in a row, with
+    norms that pass relative errors on, stay within 1e-4."""
+    _announce("block forward and backward")
+    B, N, D, H = 2, 90, 256, 4
+    names = ("x", "res", "gate", "wg", "scale", "w1", "w2", "b2")
+    shapes = ((B, N, D),) * 4 + ((D,),) * 4
+    leaves = {n: _randn(s, 20 + i, F32, 0.3 if len(s) == 1 else 1.0, 1.0 if n in ("gate", "w1", "w2", "scale") else 0.0)
+              for i, (n, s) in enumerate(zip(names, shapes))}
+    dy, dr = _randn((B, N, D), 40), _randn((B, N, D), 41)
+    t64 = {n: v.double().requires_grad_() for n, v in leaves.items()}
+    y, r2 = _torch_block(*[t64[n] for n in names], "sigmoid")
+    want = dict(zip(names, torch.autograd.grad([y, r2], [t64[n] for n in names], [dy.double(), dr.double()])))
+
+    p = {n: v.to(DEV) for n, v in leaves.items()}
+    n1, n2 = ret.Norm(EPS, p["w1"], rms=True), ret.GroupNorm(EPS, p["w2"], p["b2"])
+    heads = lambda t: t.view(B, N, H, D // H).transpose(1, 2)  # noqa: E731
+    y1, r1 = ret.residual_norm(p["x"], p["res"], n1)
+    h, _ = ret.gated_recurrence(y1, p["gate"])
+    m = torch.empty_like(h)
+    ret.gated_norm(heads(h), heads(p["wg"]), n2, out=heads(m))
+    y2, r = ret.residual_norm(m, r1, n1, scale=p["scale"])
+    dm, dr1, dscale, dw1b, _ = ret.residual_norm_backward(dy.to(DEV), r, n1, grad_r=dr.to(DEV), x=m, scale=p["scale"])
+    dh, dwg = torch.empty_like(h), torch.empty_like(h)
+    _, _, dw2, db2 = ret.gated_norm_backward(heads(dm), heads(h), heads(p["wg"]), n2, grads=(heads(dh), heads(dwg)))
+    dy1, dgate, _ = ret.gated_recurrence_backward(dh, y1, p["gate"], h)
+    dx, dres, _, dw1a, _ = ret.residual_norm_backward(dy1, r1, n1, grad_r=dr1)
+    torch.cuda.synchronize()
+    got = dict(x=dx, res=dres, gate=dgate, wg=dwg, scale=dscale, w1=dw1a + dw1b, w2=dw2, b2=db2)
+    for name, ref in (("y", y), ("r", r2)):
+        val = orc.f64(y2 if name == "y" else r)
+        np.testing.assert_allclose(val, ref.detach().numpy(), rtol=0, atol=1e-4 * ref.abs().max().item(), err_msg=name)
+    for name in names:
+        ref = want[name].numpy()
+        np.testing.assert_allclose(orc.f64(got[name]), ref, rtol=0, atol=1e-4 * np.abs(ref).max(), err_msg=name)
+
+
+def test_captured_and_replayed():
+    """A block's forward and backward in one graph with its own workspaces, replayed on new inputs between eager calls of
+    the same operators: every replay gives the eager results bit for bit."""
+    _announce("graph")
+    B, N, D = 1, 3000, 128
+    x, g, dh = _randn((B, N, D), 1, BF16).to(DEV), _gate((B, N, D), 2, BF16, "sigmoid").to(DEV), _randn((B, N, D), 3, BF16).to(DEV)
+    w = torch.ones(D, device=DEV)
+    norm = ret.Norm(EPS, w, rms=True)
+
+    def block():
+        h, s = ret.gated_recurrence(x, g, state_out=True)
+        y, r = ret.residual_norm(h, x, norm)
+        back = ret.residual_norm_backward(dh, r, norm, grad_r=x)
+        dx, dg, _ = ret.gated_recurrence_backward(back[0], x, g, h, grad_state_out=s)
+        step = ret.gated_recurrence_step(x[:, 0], g[:, 0], s)
+        return [h, s, y, r, back[0], back[3], dx, dg, step]
+
+    block()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = block()
+    for i in range(4):
+        x.copy_(_randn((B, N, D), 50 + i, BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = block()
+        torch.cuda.synchronize()
+        for k, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (i, k)
+
+
+def test_large_offsets():
+    """Rows whose element offsets pass 2^31: the last rows of a tall strided tensor, checked on their own."""
+    _announce("offsets past 2^31")
+    N, D, pitch = 1100, 64, 2_000_000
+    wide = torch.empty(N, pitch, dtype=BF16, device=DEV)
+    x = wide[:, :D].unsqueeze(0)
+    assert (N - 1) * pitch > 2 ** 31
+    vals, g = _randn((1, N, D), 1, BF16), _gate((1, N, D), 2, BF16, "sigmoid")
+    x.copy_(vals)
+    h, _ = ret.gated_recurrence(x, g.to(DEV))
+    ref, e = orc.recurrence(vals, g, "sigmoid")[0], orc.recurrence_error(vals, g, "sigmoid")[0]
+    _check(h, ref, e, "h")
+    y, _ = ret.residual_norm(x, h, ret.Norm(EPS))
+    y2, _ = ret.residual_norm(x.contiguous(), h, ret.Norm(EPS))
+    assert torch.equal(y, y2)
