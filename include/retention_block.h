@@ -63,7 +63,8 @@ enum retention_gate_form {
  * cu_seqlens[s + 1] of the one row; max_len bounds the length of a sequence.
  * A sequence may be empty (its state passes through). Tokens outside every
  * sequence, or beyond max_len of one, are neither read nor written. Offsets
- * outside [0, N] are clamped into it. Without cu_seqlens (NULL) `sequences`
+ * outside [0, N] are clamped into it. d <= 2^20 and token strides (stride_n)
+ * below 2^24 elements, else RET_ERR_UNSUPPORTED. Without cu_seqlens (NULL) `sequences`
  * must be B and max_len N.
  *
  * workspace: retention_gated_recurrence_workspace_bytes(...) bytes, 8-byte

@@ -24,15 +24,51 @@ struct Sequences {
   const int* cu;  // device [S + 1] or nullptr
 };
 
-// Planning of a recurrence call: a pure function of the sizes.
+// Planning of a recurrence call: a pure function of the sizes. A unit is a
+// sequence's (or head's) slab of kScanChannels channels; it is cut into tiles
+// of `rows` tokens, one workgroup of `waves` waves of `wave_rows` tokens each.
+// With more than one tile the workspace holds, per unit, a ticket and, per
+// tile and channel, what the tile passes on (recurrence.hip). Lanes take `vec`
+// channels, 16 bytes of them, or one where the whole row is shorter.
+constexpr int kScanChannels = 64;
+constexpr int kScanMaxWaves = 8;
+constexpr int kScanRows = 32;         // of a wave
+constexpr int kScanSigmoidBackRows = 16;  // of a wave of the sigmoid form's backward
+constexpr int kScanNarrowRows = 8;    // of a wave with one channel a lane
 struct ScanPlan {
+  int vec, waves, wave_rows, rows;
+  int64_t units, tiles;
   int64_t blocks;  // workgroups of the launch
   size_t bytes;    // workspace
 };
-inline ScanPlan plan_scan(int S, int H, int /*max_len*/, int d) {
+// Workgroups of four waves where there are many units, of eight where there
+// are few. With many, most of the tiles in flight belong to different units
+// and wait for none of the others, and the smaller workgroups keep loads and
+// stores of different ones side by side; with few, the tiles of a unit wait
+// for one another, and half as many of them, twice as long, wait less. Forward,
+// bf16, us at four and at eight: 512 units (8 x 8192 x 4096) 307 and 335, 256
+// units (4 x 8192 x 4096) 153 and 152, 32 units (65536 x 2048) 186 and 174, 4
+// units (32768 x 256) 29 and 21. Backward, log form: 256 units 257 and 311, 32
+// units 294 and 362, 1 unit (65536 x 64) 37 and 24.
+// The sigmoid form's backward reads four tensors; waves of 16 tokens let it
+// hold them in 128 registers, four waves to a SIMD: 605 us against 705 with 32
+// at 8 x 8192 x 4096.
+inline ScanPlan plan_scan(int S, int H, int max_len, int d, int dtype, bool backward, int form) {
   ScanPlan p{};
-  p.blocks = static_cast<int64_t>(S) * H * ((d + 63) / 64);
-  p.bytes = 0;
+  p.vec = dtype == 0 ? 4 : 8;
+  if (d < p.vec) p.vec = 1;
+  p.units = static_cast<int64_t>(S) * H * ((d + kScanChannels - 1) / kScanChannels);
+  p.wave_rows = p.vec == 1 ? kScanNarrowRows : backward && form == 0 ? kScanSigmoidBackRows : kScanRows;
+  const int64_t many = backward && form != 0 ? 16 : 256;
+  const int64_t most = p.units >= many ? kScanMaxWaves / 2 : kScanMaxWaves;
+  const int64_t waves = (static_cast<int64_t>(max_len) + p.wave_rows - 1) / p.wave_rows;
+  p.waves = static_cast<int>(waves < most ? waves : most);
+  p.rows = p.waves * p.wave_rows;
+  p.tiles = (static_cast<int64_t>(max_len) + p.rows - 1) / p.rows;
+  p.blocks = p.units > (int64_t{1} << 40) ? p.units : p.units * p.tiles;
+  if (p.tiles > 1)
+    p.bytes = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
+              static_cast<size_t>(p.blocks) * kScanChannels * (sizeof(uint64_t) + sizeof(uint32_t));
   return p;
 }
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,

@@ -15,6 +15,7 @@ using ret::View;
 
 constexpr int64_t kMaxSpan = int64_t{1} << 46;  // elements a view may span
 constexpr int kMaxChannels = 1 << 20;           // d of the recurrence
+constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // elements; offsets within a wave's tokens are 32-bit
 constexpr int64_t kMaxBlocks = int64_t{1} << 30;
 
 int status_of(hipError_t e) { return e == hipSuccess ? RET_OK : RET_ERR_HIP; }
@@ -133,6 +134,19 @@ int check_float_array(const float* p, int64_t n, Range* r) {
   return RET_OK;
 }
 
+// The largest of what the recurrence and its backward need in either form: one
+// workspace serves them all. 0 blocks where a launch would be out of range.
+ret::ScanPlan plan_any(int sequences, int H, int max_len, int d, int dtype) {
+  ret::ScanPlan most{};
+  for (int i = 0; i < 4; ++i) {
+    const ret::ScanPlan p = ret::plan_scan(sequences, H, max_len, d, dtype, i & 1, i >> 1);
+    if (p.blocks > kMaxBlocks) return ret::ScanPlan{};
+    most.blocks = most.blocks > p.blocks ? most.blocks : p.blocks;
+    most.bytes = most.bytes > p.bytes ? most.bytes : p.bytes;
+  }
+  return most;
+}
+
 // The checks the recurrence and its backward share.
 int check_sequences(int B, int H, int N, int d, int form, int dtype, const int* cu, int sequences, int max_len,
                     void* workspace, size_t workspace_bytes, Sequences* q, Ranges* ranges) {
@@ -144,8 +158,8 @@ int check_sequences(int B, int H, int N, int d, int form, int dtype, const int* 
   if (misaligned(cu, 4)) return RET_ERR_INVALID_ARG;
   if (d > kMaxChannels) return RET_ERR_UNSUPPORTED;
   if (max_len > N) max_len = N;
-  const ret::ScanPlan plan = ret::plan_scan(sequences, H, max_len, d);
-  if (plan.blocks <= 0 || plan.blocks > kMaxBlocks) return RET_ERR_UNSUPPORTED;
+  const ret::ScanPlan plan = plan_any(sequences, H, max_len, d, dtype);
+  if (plan.blocks <= 0) return RET_ERR_UNSUPPORTED;
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || misaligned(workspace, 8)))
     return RET_ERR_INVALID_ARG;
   *q = Sequences{sequences, H, N, d, max_len, cu};
@@ -153,6 +167,8 @@ int check_sequences(int B, int H, int N, int d, int form, int dtype, const int* 
   ranges->output(plan.bytes > 0 ? range_of(workspace, static_cast<int64_t>(plan.bytes)) : Range{});
   return RET_OK;
 }
+
+bool far_tokens(const View& v) { return v.sn >= kMaxTokenStride; }
 
 // Adds a state pair to the ranges: `to` may be `from` itself, not part of it.
 int check_states(const float* from, const float* to, int64_t n, Ranges* ranges) {
@@ -171,8 +187,8 @@ extern "C" {
 
 size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int max_len, int d, int dtype) {
   if (sequences <= 0 || H <= 0 || max_len <= 0 || d <= 0 || d > kMaxChannels || !valid_dtype(dtype)) return 0;
-  const ret::ScanPlan plan = ret::plan_scan(sequences, H, max_len, d);
-  return plan.blocks > 0 && plan.blocks <= kMaxBlocks ? plan.bytes : 0;
+  const ret::ScanPlan plan = plan_any(sequences, H, max_len, d, dtype);
+  return plan.blocks > 0 ? plan.bytes : 0;
 }
 
 int retention_gated_recurrence(const retention_view_t* x, const retention_view_t* gate, const retention_view_t* h,
@@ -192,6 +208,7 @@ int retention_gated_recurrence(const retention_view_t* x, const retention_view_t
   ranges.input(r);
   if ((st = check_view(h, B, H, N, d, dtype, true, true, &vh, &r)) != RET_OK) return st;
   ranges.output(r);
+  if (far_tokens(vx) || far_tokens(vg) || far_tokens(vh)) return RET_ERR_UNSUPPORTED;
   st = check_states(state_in, state_out, static_cast<int64_t>(sequences) * H * d, &ranges);
   if (st != RET_OK) return st;
   if (ranges.clash()) return RET_ERR_INVALID_ARG;
@@ -224,6 +241,9 @@ int retention_gated_recurrence_backward(const retention_view_t* grad_h, const re
     if ((st = check_view(given_out[i], B, H, N, d, dtype, true, true, &out[i], &r)) != RET_OK) return st;
     ranges.output(r);
   }
+  for (const View& v : in)
+    if (far_tokens(v)) return RET_ERR_UNSUPPORTED;
+  if (far_tokens(out[0]) || far_tokens(out[1])) return RET_ERR_UNSUPPORTED;
   const int64_t states = static_cast<int64_t>(sequences) * H * d;
   if ((st = check_float_array(state_in, states, &r)) != RET_OK) return st;
   ranges.input(r);

@@ -7,15 +7,22 @@ namespace ret {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// sigmoid(g) and 1 - sigmoid(g), each to a few units in the last place: with
-// e = exp(-|g|) the smaller of the two is e / (1 + e) and the larger its
-// complement, so 1 - a keeps its digits where a is near 1. Holds for +-inf.
+// sigmoid(g) and 1 - sigmoid(g), each to a few units in the last place of its
+// own size: with e = exp(-g), a = 1 / (1 + e) and 1 - a = e a. At g = -inf the
+// product is inf * 0 and the minimum takes the 1.
 __device__ __forceinline__ void sigmoid_pair(float g, float& a, float& one_less) {
-  const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(g));
-  const float small = e * __builtin_amdgcn_rcpf(1.0f + e);
-  const float large = 1.0f - small;
-  a = g >= 0.0f ? large : small;
-  one_less = g >= 0.0f ? small : large;
+  const float e = __builtin_amdgcn_exp2f(-kLog2e * g);
+  a = __builtin_amdgcn_rcpf(1.0f + e);
+  one_less = __builtin_fminf(e * a, 1.0f);
+}
+
+// Workgroup barrier that orders LDS accesses only: outstanding global loads
+// and stores stay in flight across it.
+__device__ __forceinline__ void lds_only_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 }  // namespace ret

@@ -7,25 +7,38 @@
 //   sigmoid form: dx = (1 - a) u, dg = a (1 - a) (h_{t-1} - x_t) u
 //   log form:     dx = u,         dg = a h_{t-1} u
 //
-// One thread walks the tokens of one channel.
+// Both directions are the linear recurrence y_t = a_t y_{t-1} + b_t (backward:
+// y = w, b = a dh, tokens taken from the last), bound by HBM: 3 values per
+// token and channel forward, 5 or 6 backward, about 10 flops each. A workgroup
+// takes a tile of tokens of 64 channels, reads it once into registers and
+// writes its outputs once; what the tokens before it contribute reaches it
+// through a few words per tile:
+//   - a lane holds V neighbouring channels (one 16-byte access where
+//     alignment allows) of R = 32 / V consecutive tokens, and folds them into
+//     (A, Y): y_out = A y_in + Y; pairs of folds join by
+//     (A1, Y1) then (A2, Y2) = (A1 A2, A2 Y1 + Y2);
+//   - the 64 / (64 / V) = V groups of lanes that hold the same channels at
+//     consecutive tokens join theirs through lane exchanges, the waves of the
+//     workgroup theirs through LDS;
+//   - the tile's own fold is published, then the carry into the tile is
+//     gathered from the folds of the tiles before it, back to the nearest one
+//     whose finished state is published, and the tile's own finished state
+//     follows. Tiles of a unit are handed out by a ticket, in order, so every
+//     tile that is waited for is already running, and tile 0 waits for none;
+//   - each lane then runs its tokens again from its carry, which is in order
+//     and in fp32, and rounds its outputs once.
+// Published words hold their own "not there yet" value (all ones, written by
+// scan_fill_kernel before each launch), so one relaxed access is enough.
 #include "block.h"
 #include "gate.h"
+#include "pack.h"
 
 namespace ret {
 
 namespace {
 
 constexpr int kThreads = 64;
-
-template <int FORM>
-__device__ __forceinline__ void gate_of(float g, float& a, float& c) {
-  if (FORM == 0) {
-    sigmoid_pair(g, a, c);
-  } else {
-    a = __builtin_amdgcn_exp2f(kLog2e * g);
-    c = 1.0f;
-  }
-}
+constexpr uint32_t kXcds = 8;
 
 struct Piece {
   int64_t first;  // its first token in the row
@@ -45,61 +58,496 @@ __device__ __forceinline__ T* row_of(const View& v, int b, int h) {
   return reinterpret_cast<T*>(v.data) + b * v.sb + h * v.sh;
 }
 
-template <typename T, int FORM>
-__global__ void __launch_bounds__(kThreads)
-recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_in, float* state_out) {
-  const int slabs = (q.d + kThreads - 1) / kThreads;
-  const int64_t sh = blockIdx.x / slabs;
-  const int c = (blockIdx.x % slabs) * kThreads + threadIdx.x;
-  const int s = static_cast<int>(sh / q.H), h = static_cast<int>(sh % q.H);
-  if (c >= q.d) return;
-  const Piece p = piece_of(q, s);
-  const T* xr = row_of<T>(x, p.b, h) + p.first * x.sn + c;
-  const T* gr = row_of<T>(gate, p.b, h) + p.first * gate.sn + c;
-  T* hr = row_of<T>(out, p.b, h) + p.first * out.sn + c;
-  float now = state_in ? state_in[sh * q.d + c] : 0.0f;
-  for (int t = 0; t < p.len; ++t) {
-    float a, w;
-    gate_of<FORM>(Elem<T>::load(gr, t * gate.sn), a, w);
-    now = fmaf(a, now, w * Elem<T>::load(xr, t * x.sn));
-    Elem<T>::store(hr, t * out.sn, now);
+template <int FORM>
+__device__ __forceinline__ void gate_of(float g, float& a, float& c) {
+  if (FORM == 0) {
+    sigmoid_pair(g, a, c);
+  } else {
+    a = __builtin_amdgcn_exp2f(kLog2e * g);
+    c = 1.0f;
   }
-  if (state_out) state_out[sh * q.d + c] = now;
 }
 
-template <typename T, int FORM>
-__global__ void __launch_bounds__(kThreads)
-recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
-                           const float* state_in, const float* grad_state_out, float* grad_state_in) {
-  const int slabs = (q.d + kThreads - 1) / kThreads;
-  const int64_t sh = blockIdx.x / slabs;
-  const int c = (blockIdx.x % slabs) * kThreads + threadIdx.x;
-  const int s = static_cast<int>(sh / q.H), h = static_cast<int>(sh % q.H);
-  if (c >= q.d) return;
-  const Piece p = piece_of(q, s);
-  const T* dr = row_of<T>(grad_h, p.b, h) + p.first * grad_h.sn + c;
-  const T* xr = FORM == 0 ? row_of<T>(x, p.b, h) + p.first * x.sn + c : nullptr;
-  const T* gr = row_of<T>(gate, p.b, h) + p.first * gate.sn + c;
-  const T* hr = row_of<T>(hv, p.b, h) + p.first * hv.sn + c;
-  T* dxr = row_of<T>(grad_x, p.b, h) + p.first * grad_x.sn + c;
-  T* dgr = row_of<T>(grad_gate, p.b, h) + p.first * grad_gate.sn + c;
-  const float start = state_in ? state_in[sh * q.d + c] : 0.0f;
-  float w = grad_state_out ? grad_state_out[sh * q.d + c] : 0.0f;
-  for (int t = p.len - 1; t >= 0; --t) {
-    float a, keep;
-    gate_of<FORM>(Elem<T>::load(gr, t * gate.sn), a, keep);
-    const float u = Elem<T>::load(dr, t * grad_h.sn) + w;
-    const float before = t > 0 ? Elem<T>::load(hr, (t - 1) * hv.sn) : start;
-    if (FORM == 0) {
-      Elem<T>::store(dxr, t * grad_x.sn, keep * u);
-      Elem<T>::store(dgr, t * grad_gate.sn, a * keep * (before - Elem<T>::load(xr, t * x.sn)) * u);
-    } else {
-      Elem<T>::store(dxr, t * grad_x.sn, u);
-      Elem<T>::store(dgr, t * grad_gate.sn, a * before * u);
-    }
-    w = a * u;
+// The workspace of a launch with more than one tile.
+struct ScanWords {
+  uint32_t* ticket;  // [units], from all ones up
+  uint64_t* fold;    // [units][tiles][64]: Y, A
+  uint32_t* state;   // [units][tiles][64]: the state after the tile
+};
+
+__global__ void __launch_bounds__(256) scan_fill_kernel(uint64_t* words, int64_t n) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+    words[i] = ~uint64_t{0};
+}
+
+__device__ __forceinline__ void publish(uint32_t* at, float v) {
+  const uint32_t w = __float_as_uint(v);
+  __hip_atomic_store(at, w == ~0u ? 0x7fc00000u : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(uint64_t* at, float A, float Y) {
+  uint64_t w = static_cast<uint64_t>(__float_as_uint(Y)) << 32 | __float_as_uint(A);
+  if (w == ~uint64_t{0}) w = uint64_t{0x7fc00000u} << 32 | 0x7fc00000u;
+  __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The states of 64 channels (a lane each) before `tile` > 0, from the words of
+// the tiles before it: the nearest finished state among the last kDepth, run
+// forward through the folds of the tiles since. Whichever state it starts
+// from, the arithmetic is that of going through the tiles one by one, so the
+// result does not depend on timing. Looks at the nearest tile first, then
+// kAhead at a time, the folds of the nearer ones put aside in `stash` (with
+// many units the nearest state is mostly there, and reading further tiles'
+// words for it costs 2%; four at a time cost registers: 4% of the log backward). `fold`
+// and `state` are the words of the unit's tile 0, 64 words a tile. Polls at
+// most kPolls times (about a second), then gives NaN: a wave reaches the end
+// whatever the workspace holds.
+constexpr int kAhead = 2;
+constexpr int kDepth = 32;
+constexpr int kPolls = 1 << 20;
+__device__ __forceinline__ float fold_on(uint64_t f, float y) {
+  return fmaf(__uint_as_float(static_cast<uint32_t>(f)), y, __uint_as_float(static_cast<uint32_t>(f >> 32)));
+}
+typedef uint64_t Stash[kDepth][kScanChannels];
+
+// Looks at K tiles from `tile` - 1 - depth back. True with the state before
+// `tile` in y; else depth grows by K where all K folds were there.
+template <int K>
+__device__ __forceinline__ bool look(const uint64_t* fold, const uint32_t* state, int tile, Stash& stash, int lane,
+                                     int& depth, float& y) {
+  uint32_t s[K];
+  uint64_t f[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int from = tile - 1 - depth - k;
+    const int64_t i = static_cast<int64_t>(from > 0 ? from : 0) * kScanChannels;
+    s[k] = __hip_atomic_load(state + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    f[k] = __hip_atomic_load(fold + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (grad_state_in) grad_state_in[sh * q.d + c] = w;
+  bool folds = true;  // of the tiles nearer than k, all there
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (folds && __all(s[k] != ~0u)) {
+      y = __uint_as_float(s[k]);
+#pragma unroll
+      for (int j = K - 1; j >= 0; --j)
+        if (j < k) y = fold_on(f[j], y);
+      for (int j = depth - 1; j >= 0; --j) y = fold_on(stash[j][lane], y);
+      return true;
+    }
+    folds = folds && __all(f[k] != ~uint64_t{0});  // never tile 0's, which publishes its state alone
+  }
+  if (folds && depth + K <= kDepth) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) stash[depth + k][lane] = f[k];
+    depth += K;
+  } else {
+    __builtin_amdgcn_s_sleep(1);
+  }
+  return false;
+}
+
+__device__ __forceinline__ float look_back(const uint64_t* fold, const uint32_t* state, int tile, Stash& stash,
+                                           int lane) {
+  int depth = 0;
+  float y = __uint_as_float(0x7fc00000u);
+  for (int poll = 0; poll < kPolls; ++poll) {
+    if (depth == 0 ? look<1>(fold, state, tile, stash, lane, depth, y)
+                   : look<kAhead>(fold, state, tile, stash, lane, depth, y))
+      break;
+  }
+  return y;
+}
+
+// What a workgroup shares. Channel i of the slab is fold[wave][kPad + i]; the
+// last lanes of a row whose width is no multiple of V use the places before 0.
+constexpr int kPad = 8;
+struct ScanShared {
+  float2 fold[kScanMaxWaves][kPad + kScanChannels];  // the waves' folds, then in x the carry into each wave
+  Stash stash;
+  int tile;
+};
+
+// A lane's place: V channels from `start` of the row, tokens sub * R on of its
+// wave's. The last lane of a row moves `shift` channels back to end with it;
+// the channels it shares with its neighbour are computed by both and stored by
+// the neighbour. A lane past the row (`in` false) reads the row's last channels.
+template <int V>
+struct ScanLane {
+  int wave, sub, start, shift;
+  int word;  // of the lane's first channel in ScanShared::fold[]
+  bool in;
+  __device__ __forceinline__ ScanLane(int slab, int d) {
+    constexpr int CG = kScanChannels / V;
+    const int lane = threadIdx.x & 63, cg = lane % CG;
+    const int c = slab * kScanChannels + cg * V;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    sub = lane / CG;
+    in = c < d;
+    start = c < d - V ? c : d - V;
+    shift = in ? c - start : 0;
+    word = kPad + cg * V - shift;
+  }
+};
+
+// The unit of this workgroup and the tile its number suggests. Units go round
+// the workgroups, so that those of one tile of tokens run together.
+struct ScanPlace {
+  int64_t unit, sh;
+  int h, slab, tile;
+  Piece piece;
+};
+__device__ __forceinline__ ScanPlace scan_place(const Sequences& q, uint32_t units) {
+  ScanPlace p;
+  const uint32_t block = blockIdx.x, turn = block % units;
+  // Workgroups go round the eight XCDs; neighbouring slabs go to one of them
+  // where the units can be shared out evenly, so that the rows' pieces meet in
+  // one L2: 10 to 12% faster at 8 x 8192 x 4096.
+  const uint32_t unit = units % kXcds ? turn : turn % kXcds * (units / kXcds) + turn / kXcds;
+  const uint32_t slabs = (q.d + kScanChannels - 1) / kScanChannels;
+  const uint32_t sh = unit / slabs;
+  p.unit = unit;
+  p.tile = block / units;
+  p.sh = sh;
+  p.slab = unit - sh * slabs;
+  const int s = sh / q.H;
+  p.h = sh - s * q.H;
+  p.piece = piece_of(q, s);
+  return p;
+}
+
+// The next tile of the unit.
+__device__ __forceinline__ int take_ticket(const ScanWords& w, int64_t unit, int& at) {
+  if (threadIdx.x == 0)
+    at = static_cast<int>(
+        __hip_atomic_fetch_add(w.ticket + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
+  lds_only_barrier();
+  return __builtin_amdgcn_readfirstlane(at);
+}
+
+// Joins the lanes' folds (A, Y) of the workgroup, gets the tile's carry and
+// leaves in y the state before each lane's first token. `first` and `last` are
+// the states before the sequence (may be null) and after it (null: not
+// wanted), at this unit's channel 0; `left` how many channels there are.
+template <int V>
+__device__ __forceinline__ void scan_carry(float (&A)[V], float (&Y)[V], float (&y)[V], const ScanWords& w,
+                                           const ScanPlace& p, int tiles, bool end, const float* first, float* last,
+                                           int left, const ScanLane<V>& at, ScanShared& shared) {
+  constexpr int CG = kScanChannels / V;  // lanes side by side
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  // Inclusive over the V groups of lanes.
+#pragma unroll
+  for (int off = 1; off < V; off *= 2) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float A1 = __shfl_up(A[j], off * CG, 64), Y1 = __shfl_up(Y[j], off * CG, 64);
+      if (at.sub >= off) {
+        Y[j] = fmaf(A[j], Y1, Y[j]);
+        A[j] *= A1;
+      }
+    }
+  }
+  if (at.sub == V - 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) shared.fold[at.wave][at.word + j] = make_float2(A[j], Y[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float A1 = __shfl_up(A[j], CG, 64), Y1 = __shfl_up(Y[j], CG, 64);
+    A[j] = at.sub ? A1 : 1.0f;
+    Y[j] = at.sub ? Y1 : 0.0f;
+  }
+  lds_only_barrier();
+  if (at.wave == 0) {  // a lane per channel
+    float TA = 1.0f, TY = 0.0f;
+    for (int k = 0; k < waves; ++k) {
+      const float2 g = shared.fold[k][kPad + lane];
+      TY = fmaf(g.x, TY, g.y);
+      TA *= g.x;
+    }
+    const int64_t word = p.unit * tiles * kScanChannels + lane;
+    const int64_t here = word + static_cast<int64_t>(p.tile) * kScanChannels;
+    float carry;
+    if (p.tile == 0) {
+      carry = first && lane < left ? first[lane] : 0.0f;
+    } else {
+      if (!end) publish(w.fold + here, TA, TY);
+      carry = look_back(w.fold + word, w.state + word, p.tile, shared.stash, lane);
+    }
+    const float after = fmaf(TA, carry, TY);
+    if (!end) publish(w.state + here, after);
+    else if (last && lane < left) last[lane] = after;
+    for (int k = 0; k < waves; ++k) {
+      const float2 g = shared.fold[k][kPad + lane];
+      shared.fold[k][kPad + lane].x = carry;
+      carry = fmaf(g.x, carry, g.y);
+    }
+  }
+  lds_only_barrier();
+#pragma unroll
+  for (int j = 0; j < V; ++j) y[j] = fmaf(A[j], shared.fold[at.wave][at.word + j].x, Y[j]);
+}
+
+// Stores a lane's channels: all V, or the last V - shift of them.
+template <typename T, int V>
+__device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const ScanLane<V>& at) {
+  if (!at.in) return;
+  if (at.shift == 0) {
+    Pack<T, V>::store(p, x);
+  } else {
+#pragma unroll
+    for (int j = 1; j < V; ++j)
+      if (j >= at.shift) Elem<T>::store(p, j, x[j]);
+  }
+}
+
+template <typename T, int FORM, int V, int E>
+__global__ void __launch_bounds__(64 * kScanMaxWaves, 4)
+recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_in, float* state_out, ScanWords w,
+                  uint32_t units, int tiles) {
+  __shared__ ScanShared shared;
+  constexpr int R = E / V;
+  typedef Pack<T, V> P;
+  const int rows = static_cast<int>(blockDim.x >> 6) * E;
+  ScanPlace p = scan_place(q, units);
+  const ScanLane<V> at(p.slab, q.d);
+  const int len = p.piece.len;
+  const T* xr = row_of<T>(x, p.piece.b, p.h) + p.piece.first * x.sn;
+  const T* gr = row_of<T>(gate, p.piece.b, p.h) + p.piece.first * gate.sn;
+
+  typename P::raw xw[R], gw[R];
+  auto load = [&](int tile) {
+    const int64_t row = static_cast<int64_t>(tile) * rows;  // below len
+    if (row + rows <= len) {
+      const T* xb = xr + (row + at.wave * E) * x.sn;
+      const T* gb = gr + (row + at.wave * E) * gate.sn;
+      const uint32_t xo = at.sub * R * static_cast<uint32_t>(x.sn) + at.start;
+      const uint32_t go = at.sub * R * static_cast<uint32_t>(gate.sn) + at.start;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        gw[i] = P::load(gb + i * gate.sn + go);
+        xw[i] = P::load(xb + i * x.sn + xo);
+      }
+    } else {  // tokens past the end read the last one
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        int64_t t = row + at.wave * E + at.sub * R + i;
+        t = t < len ? t : len - 1;
+        gw[i] = P::load(gr + t * gate.sn + at.start);
+        xw[i] = P::load(xr + t * x.sn + at.start);
+      }
+    }
+  };
+  // The loads start for the suggested tile while the ticket is on its way.
+  if (static_cast<int64_t>(p.tile) * rows < len) load(p.tile);
+  if (tiles > 1) {
+    const int tile = take_ticket(w, p.unit, shared.tile);
+    if (tile >= tiles) return;
+    if (tile != p.tile) {
+      p.tile = tile;
+      if (static_cast<int64_t>(tile) * rows < len) load(tile);
+    }
+  }
+  const int64_t row0 = static_cast<int64_t>(p.tile) * rows;
+  if (p.tile > 0 && row0 >= len) return;
+  const int64_t t0 = row0 + at.wave * E + at.sub * R;
+  const bool full = row0 + rows <= len;
+
+  float a[R][V], b[R][V];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    P::unpack(gw[i], a[i]);
+    P::unpack(xw[i], b[i]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (FORM == 0) {
+        float keep;
+        sigmoid_pair(a[i][j], a[i][j], keep);
+        b[i][j] *= keep;
+      } else {
+        a[i][j] = __builtin_amdgcn_exp2f(kLog2e * a[i][j]);
+      }
+    }
+  }
+  if (!full) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t0 + i < len) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        a[i][j] = 1.0f;
+        b[i][j] = 0.0f;
+      }
+    }
+  }
+  float A[V], Y[V], y[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    A[j] = a[0][j];
+    Y[j] = b[0][j];
+#pragma unroll
+    for (int i = 1; i < R; ++i) {
+      Y[j] = fmaf(a[i][j], Y[j], b[i][j]);
+      A[j] *= a[i][j];
+    }
+  }
+  const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
+  scan_carry<V>(A, Y, y, w, p, tiles, row0 + rows >= len, state_in ? state_in + unit_state : nullptr,
+                state_out ? state_out + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
+  T* hr = row_of<T>(out, p.piece.b, p.h) + p.piece.first * out.sn;
+  if (full) {
+    T* hb = hr + (row0 + at.wave * E) * out.sn;
+    const uint32_t ho = at.sub * R * static_cast<uint32_t>(out.sn) + at.start;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
+      store_channels<T, V>(hb + i * out.sn + ho, y, at);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
+      if (t0 + i < len) store_channels<T, V>(hr + (t0 + i) * out.sn + at.start, y, at);
+    }
+  }
+}
+
+// The same from the last token on: token t of the recurrence is row
+// len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
+// are needed after the carry only and stay in flight until then.
+template <typename T, int FORM, int V, int E>
+__global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 ? 4 : 2)
+recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
+                           const float* state_in, const float* grad_state_out, float* grad_state_in, ScanWords w,
+                           uint32_t units, int tiles) {
+  __shared__ ScanShared shared;
+  constexpr int R = E / V;
+  typedef Pack<T, V> P;
+  const int rows = static_cast<int>(blockDim.x >> 6) * E;
+  ScanPlace p = scan_place(q, units);
+  const ScanLane<V> at(p.slab, q.d);
+  const int len = p.piece.len;
+  auto row = [&](const View& v) { return row_of<T>(v, p.piece.b, p.h) + p.piece.first * v.sn; };
+  const T *dr = row(grad_h), *gr = row(gate), *hr = row(hv), *xr = FORM == 0 ? row(x) : nullptr;
+
+  typename P::raw xw[R], hw[R], gw[R], dw[R];
+  // A tile's tokens and the one before them all exist where row + rows < len.
+  auto load = [&](int tile) {
+    const int64_t t = static_cast<int64_t>(tile) * rows;  // below len
+    if (t + rows < len) {
+      const int64_t low = len - (t + at.wave * E + E);  // the wave's first row in memory
+      const uint32_t lane_row = (V - 1 - at.sub) * R;
+      auto get = [&](const T* from, int64_t sn, typename P::raw (&to)[R], int64_t back) {
+        const T* base = from + (low - back) * sn;
+        const uint32_t o = lane_row * static_cast<uint32_t>(sn) + at.start;
+#pragma unroll
+        for (int i = 0; i < R; ++i) to[i] = P::load(base + (R - 1 - i) * sn + o);
+      };
+      get(gr, gate.sn, gw, 0);
+      get(dr, grad_h.sn, dw, 0);
+      get(hr, hv.sn, hw, 1);
+      if (FORM == 0) get(xr, x.sn, xw, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        int64_t r = len - 1 - (t + at.wave * E + at.sub * R + i);
+        r = r > 0 ? r : 0;
+        gw[i] = P::load(gr + r * gate.sn + at.start);
+        dw[i] = P::load(dr + r * grad_h.sn + at.start);
+        hw[i] = P::load(hr + (r > 0 ? r - 1 : 0) * hv.sn + at.start);
+        if (FORM == 0) xw[i] = P::load(xr + r * x.sn + at.start);
+      }
+    }
+  };
+  if (static_cast<int64_t>(p.tile) * rows < len) load(p.tile);
+  if (tiles > 1) {
+    const int tile = take_ticket(w, p.unit, shared.tile);
+    if (tile >= tiles) return;
+    if (tile != p.tile) {
+      p.tile = tile;
+      if (static_cast<int64_t>(tile) * rows < len) load(tile);
+    }
+  }
+  const int64_t row0 = static_cast<int64_t>(p.tile) * rows;
+  if (p.tile > 0 && row0 >= len) return;
+  const int64_t t0 = row0 + at.wave * E + at.sub * R;
+  const bool full = row0 + rows < len;
+
+  // In the sigmoid form a decay near 1 is held as its negated distance from 1,
+  // which has more digits, and any other as it is.
+  auto decay = [](float v) { return FORM == 0 && __float_as_int(v) < 0 ? 1.0f + v : v; };
+  auto rest = [](float v) { return __float_as_int(v) < 0 ? -v : 1.0f - v; };
+  float a[R][V], dh[R][V];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    P::unpack(gw[i], a[i]);
+    P::unpack(dw[i], dh[i]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (FORM == 0) {
+        float keep, d;
+        sigmoid_pair(a[i][j], d, keep);
+        a[i][j] = d > 0.5f ? -keep : d;
+      } else {
+        a[i][j] = __builtin_amdgcn_exp2f(kLog2e * a[i][j]);
+      }
+    }
+  }
+  if (!full) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t0 + i < len) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        a[i][j] = FORM == 0 ? -0.0f : 1.0f;
+        dh[i][j] = 0.0f;
+      }
+    }
+  }
+  float A[V], Y[V], y[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    A[j] = 1.0f;
+    Y[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float d = decay(a[i][j]);
+      Y[j] = d * (Y[j] + dh[i][j]);
+      A[j] *= d;
+    }
+  }
+  const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
+  scan_carry<V>(A, Y, y, w, p, tiles, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
+                grad_state_in ? grad_state_in + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
+  T *dxr = row(grad_x), *dgr = row(grad_gate);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = len - 1 - (t0 + i);
+    float before[V], v[V], dx[V], dg[V];
+    P::unpack(hw[i], before);
+    if (FORM == 0) P::unpack(xw[i], v);
+    if (!full && r == 0) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) before[j] = state_in ? state_in[p.sh * q.d + at.start + j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = decay(a[i][j]), u = dh[i][j] + y[j];
+      y[j] = d * u;
+      if (FORM == 0) {
+        dx[j] = rest(a[i][j]) * u;
+        dg[j] = d * (before[j] - v[j]) * dx[j];
+      } else {
+        dx[j] = u;
+        dg[j] = before[j] * y[j];
+      }
+    }
+    if (full || r >= 0) {
+      store_channels<T, V>(dxr + r * grad_x.sn + at.start, dx, at);
+      store_channels<T, V>(dgr + r * grad_gate.sn + at.start, dg, at);
+    }
+  }
 }
 
 // Grid: x over the channels of a row (H * d), y-strided over the B rows. A
@@ -147,21 +595,82 @@ step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int
     }                                                                                  \
   } while (0)
 
+namespace {
+
+// Fills the words of a launch with several tiles; *words points into them.
+hipError_t scan_words(const ScanPlan& p, void* workspace, ScanWords* words, hipStream_t stream) {
+  *words = ScanWords{};
+  if (p.tiles <= 1) return hipSuccess;
+  char* base = static_cast<char*>(workspace);
+  words->ticket = reinterpret_cast<uint32_t*>(base);
+  base += (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256;
+  words->fold = reinterpret_cast<uint64_t*>(base);
+  words->state = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(p.blocks) * kScanChannels * sizeof(uint64_t));
+  const int64_t n = static_cast<int64_t>(p.bytes / sizeof(uint64_t));
+  const int64_t blocks = (n + 255) / 256;
+  scan_fill_kernel<<<static_cast<unsigned>(blocks < 2048 ? blocks : 2048), 256, 0, stream>>>(
+      reinterpret_cast<uint64_t*>(workspace), n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,
-                                   const Sequences& q, const float* state_in, float* state_out, void*,
+                                   const Sequences& q, const float* state_in, float* state_out, void* workspace,
                                    hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(plan_scan(q.S, q.H, q.max_len, q.d).blocks));
-  RET_BY_FORM_AND_TYPE(recurrence_kernel, x, gate, h, q, state_in, state_out);
+  const ScanPlan p = plan_scan(q.S, q.H, q.max_len, q.d, dtype, false, form);
+  ScanWords words;
+  const hipError_t e = scan_words(p, workspace, &words, stream);
+  if (e != hipSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
+#define RET_SCAN(T, FORM, V, E)                                                                            \
+  recurrence_kernel<T, FORM, V, E><<<grid, block, 0, stream>>>(x, gate, h, q, state_in, state_out, words, \
+                                                               static_cast<uint32_t>(p.units),            \
+                                                               static_cast<int>(p.tiles))
+#define RET_SCAN_VEC(T, FORM, V)                            \
+  do {                                                      \
+    if (p.vec == V) RET_SCAN(T, FORM, V, kScanRows);        \
+    else RET_SCAN(T, FORM, 1, kScanNarrowRows);             \
+  } while (0)
+  if (dtype == 0) {
+    if (form == 0) RET_SCAN_VEC(float, 0, 4);
+    else RET_SCAN_VEC(float, 1, 4);
+  } else {
+    if (form == 0) RET_SCAN_VEC(uint16_t, 0, 8);
+    else RET_SCAN_VEC(uint16_t, 1, 8);
+  }
+#undef RET_SCAN_VEC
+#undef RET_SCAN
   return hipGetLastError();
 }
 
 hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& grad_h, const View& x, const View& gate,
                                             const View& h, const View& grad_x, const View& grad_gate,
                                             const Sequences& q, const float* state_in, const float* grad_state_out,
-                                            float* grad_state_in, void*, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(plan_scan(q.S, q.H, q.max_len, q.d).blocks));
-  RET_BY_FORM_AND_TYPE(recurrence_backward_kernel, grad_h, x, gate, h, grad_x, grad_gate, q, state_in, grad_state_out,
-                       grad_state_in);
+                                            float* grad_state_in, void* workspace, hipStream_t stream) {
+  const ScanPlan p = plan_scan(q.S, q.H, q.max_len, q.d, dtype, true, form);
+  ScanWords words;
+  const hipError_t e = scan_words(p, workspace, &words, stream);
+  if (e != hipSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
+#define RET_SCAN(T, FORM, V, E)                                                                                \
+  recurrence_backward_kernel<T, FORM, V, E><<<grid, block, 0, stream>>>(                                       \
+      grad_h, x, gate, h, grad_x, grad_gate, q, state_in, grad_state_out, grad_state_in, words,                \
+      static_cast<uint32_t>(p.units), static_cast<int>(p.tiles))
+#define RET_SCAN_VEC(T, FORM, V, E)                        \
+  do {                                                     \
+    if (p.vec == V) RET_SCAN(T, FORM, V, E);               \
+    else RET_SCAN(T, FORM, 1, kScanNarrowRows);            \
+  } while (0)
+  if (dtype == 0) {
+    if (form == 0) RET_SCAN_VEC(float, 0, 4, kScanSigmoidBackRows);
+    else RET_SCAN_VEC(float, 1, 4, kScanRows);
+  } else {
+    if (form == 0) RET_SCAN_VEC(uint16_t, 0, 8, kScanSigmoidBackRows);
+    else RET_SCAN_VEC(uint16_t, 1, 8, kScanRows);
+  }
+#undef RET_SCAN_VEC
+#undef RET_SCAN
   return hipGetLastError();
 }
 

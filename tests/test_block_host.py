@@ -119,6 +119,7 @@ def test_recurrence_refuses(lib, kw):
 def test_recurrence_limits(lib):
     assert recurrence(lib, B=1 << 16, H=1 << 10, N=1 << 10) == UNSUPPORTED
     assert recurrence(lib, d=(1 << 20) + 1) == UNSUPPORTED
+    assert recurrence(lib, strides=(1 << 34, 1 << 32, 1 << 24), h_strides=(19200, 6400, 64)) == UNSUPPORTED
     assert recurrence(lib, strides=(1 << 60, 6400, 64), h_strides=(19200, 6400, 64)) == UNSUPPORTED
 
 
