@@ -93,17 +93,17 @@ struct NormArgs {
 // gate.data is nullptr without a gate.
 hipError_t launch_gated_norm(int dtype, const View& o, const View& gate, const View& y, int B, int H, int N, int d,
                              const NormArgs& norm, hipStream_t stream);
-// Partial sums of the parameter gradients of `heads` heads of `rows` rows of d
-// values: `parts` workgroups per head leave `sums` rows of d floats each.
-struct ParamPlan {
-  int parts;
-  size_t bytes;
-};
-inline ParamPlan plan_params(int heads, int64_t rows, int d, int sums) {
-  ParamPlan p{};
-  p.parts = static_cast<int>(rows < 64 ? rows : 64);
-  p.bytes = static_cast<size_t>(heads) * p.parts * sums * d * sizeof(float);
-  return p;
+// Workgroups of a norm's launch, per head: as many as the rows give at
+// `at_once` rows each, at most `groups` over all heads.
+constexpr int kForwardGroups = 4096, kBackwardGroups = 1024;
+inline int norm_parts(int heads, int rows, int at_once, int groups) {
+  const int want = (rows - 1) / at_once + 1, most = (groups + heads - 1) / heads;
+  return want < most ? want : most;
+}
+// Bytes of the backward's partial sums: a row of `sums` times d floats for
+// each of its workgroups (whatever the rows a workgroup takes at a time).
+inline size_t param_bytes(int heads, int rows, int d, int sums) {
+  return static_cast<size_t>(heads) * norm_parts(heads, rows, 1, kBackwardGroups) * sums * d * sizeof(float);
 }
 constexpr int kGatedNormSums = 2;     // weight, bias
 constexpr int kResidualNormSums = 3;  // scale, weight, bias

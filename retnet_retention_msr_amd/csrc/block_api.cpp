@@ -301,7 +301,7 @@ int retention_gated_norm(const retention_view_t* o, const retention_view_t* gate
 
 size_t retention_gated_norm_backward_workspace_bytes(int B, int H, int N, int d, int dtype, int with_params) {
   if (check_dims(B, H, N, d, dtype) != RET_OK || d > RETENTION_MAX_DV || H > RETENTION_MAX_HEADS || !with_params) return 0;
-  return ret::plan_params(H, static_cast<int64_t>(B) * N, d, ret::kGatedNormSums).bytes;
+  return ret::param_bytes(H, B * N, d, ret::kGatedNormSums);
 }
 
 int retention_gated_norm_backward(const retention_view_t* grad_y, const retention_view_t* o,
@@ -334,7 +334,7 @@ int retention_gated_norm_backward(const retention_view_t* grad_y, const retentio
     ranges.output(r);
   }
   if (grad_weight || grad_bias) {
-    const size_t need = ret::plan_params(H, static_cast<int64_t>(B) * N, d, ret::kGatedNormSums).bytes;
+    const size_t need = ret::param_bytes(H, B * N, d, ret::kGatedNormSums);
     if (!workspace || workspace_bytes < need || misaligned(workspace, 4)) return RET_ERR_INVALID_ARG;
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }
@@ -373,7 +373,7 @@ int retention_residual_norm(const retention_view_t* x, const retention_view_t* r
 
 size_t retention_residual_norm_backward_workspace_bytes(int B, int N, int D, int dtype, int with_params) {
   if (check_dims(B, 1, N, D, dtype) != RET_OK || D > RETENTION_MAX_MODEL_DIM || !with_params) return 0;
-  return ret::plan_params(1, static_cast<int64_t>(B) * N, D, ret::kResidualNormSums).bytes;
+  return ret::param_bytes(1, B * N, D, ret::kResidualNormSums);
 }
 
 int retention_residual_norm_backward(const retention_view_t* grad_y, const retention_view_t* grad_r,
@@ -411,7 +411,7 @@ int retention_residual_norm_backward(const retention_view_t* grad_y, const reten
     ranges.output(g);
   }
   if (grad_scale || grad_weight || grad_bias) {
-    const size_t need = ret::plan_params(1, static_cast<int64_t>(B) * N, D, ret::kResidualNormSums).bytes;
+    const size_t need = ret::param_bytes(1, B * N, D, ret::kResidualNormSums);
     if (!workspace || workspace_bytes < need || misaligned(workspace, 4)) return RET_ERR_INVALID_ARG;
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }

@@ -7,10 +7,19 @@
 //   dv = rstd (q - mean(q) - xhat mean(q xhat)), q the gradient of xhat
 // (without mean(q) in the rms form). Parameter gradients are sums over rows.
 //
-// One workgroup of 256 threads takes a row at a time and reads it again for
-// each pass over it.
+// Every operator here reads its tensors once and writes its results once and
+// is bound by HBM. A row is held in the registers of L lanes, at most 16
+// values each: part of a wave for narrow heads (several rows to a wave), a
+// wave up to 1024 values, a workgroup beyond. Its statistics are sums over
+// registers, then lane exchanges, then, across waves, one exchange through
+// LDS; the backward forms them again from the row it has to read anyway, so
+// nothing but the forward's input is kept. Threads stay with their channels
+// and go over the rows, holding the weights, and the parameters' sums in the
+// backward, in registers; each workgroup leaves one row of partial sums, which
+// a second kernel adds in a fixed order.
 #include "block.h"
 #include "gate.h"
+#include "pack.h"
 
 namespace ret {
 
@@ -18,259 +27,652 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Mean and 1 / deviation of a row given by load(c), c < d.
-template <typename F>
-__device__ __forceinline__ void row_stats(F load, int d, const NormArgs& n, float* red, float& mean, float& rstd) {
-  mean = 0.0f;
+// ---------------------------------------------------------------------------
+// Sums over the L lanes of a row
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over each aligned group of L <= 64 lanes, in every lane: neighbours,
+// pairs, fours (mirrored within 8), eights (mirrored within 16), then the
+// 16-lane rows and the two halves exchanged.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+  if constexpr (L >= 2) x += dpp<0xB1>(x);
+  if constexpr (L >= 4) x += dpp<0x4E>(x);
+  if constexpr (L >= 8) x += dpp<0x141>(x);
+  if constexpr (L >= 16) x += dpp<0x140>(x);
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// A thread's part of a row
+
+// K chunks of V neighbouring channels, L threads side by side. With MASK the
+// row may end anywhere: a chunk that crosses its end is moved back to end with
+// it, its first lo[k] channels belonging to the neighbour (V of them, all, for
+// a chunk past the end).
+template <int L, int V, int K, bool MASK>
+struct Part {
+  static constexpr int E = V * K;
+  int start[K], lo[K];
+  __device__ __forceinline__ explicit Part(int lane, int d) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * L + lane) * V;
+      start[k] = MASK && c > d - V ? d - V : c;
+      lo[k] = !MASK ? 0 : c < d ? c - start[k] : V;
+    }
+  }
+  __device__ __forceinline__ bool own(int k, int j) const { return !MASK || j >= lo[k]; }
+
+  // Values of the row at p (0 for channels that are not the thread's own).
+  template <typename T>
+  struct Raw {
+    typename Pack<T, V>::raw w[K];
+  };
+  template <typename T>
+  __device__ __forceinline__ Raw<T> load(const T* p) const {
+    Raw<T> r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) r.w[k] = Pack<T, V>::load(p + start[k]);
+    return r;
+  }
+  template <typename T>
+  __device__ __forceinline__ void values(const Raw<T>& r, float (&x)[E]) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[V];
+      Pack<T, V>::unpack(r.w[k], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[k * V + j] = own(k, j) ? v[j] : 0.0f;
+    }
+  }
+  // Parameters at p, or `none`.
+  __device__ __forceinline__ void params(const float* p, float none, float (&x)[E]) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[V];
+      if (p) Pack<float, V>::unpack(Pack<float, V>::load(p + start[k]), v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[k * V + j] = p ? v[j] : none;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, const float (&x)[E]) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = x[k * V + j];
+      if (!MASK || lo[k] == 0) {
+        Pack<T, V>::store(p + start[k], v);
+      } else {
+#pragma unroll
+        for (int j = 1; j < V; ++j)
+          if (j >= lo[k]) Elem<T>::store(p + start[k], j, v[j]);
+      }
+    }
+  }
+  // Adds what is the thread's own to the float row at p.
+  __device__ __forceinline__ void put(float* p, const float (&x)[E]) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (own(k, j)) p[start[k] + j] = x[k * V + j];
+  }
+  // How many channels of the row wave `w` holds.
+  static __device__ __forceinline__ int count(int w, int d) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int left = d - (k * L + w * 64) * V;
+      n += left < 0 ? 0 : left < 64 * V ? left : 64 * V;
+    }
+    return n;
+  }
+};
+
+// What the waves of a row exchange: [0] its moments (two sets, used in turn),
+// [1] the backward's two sums.
+template <int L>
+struct RowShared {
+  float2 moment[2][L / 64 > 0 ? L / 64 : 1];
+  float2 sums[L / 64 > 0 ? L / 64 : 1];
+};
+
+// Mean and 1 / deviation of a row. Across waves each wave's sum and squared
+// deviations from its own mean are joined: M2 = sum M2_w + n_w (mean_w - mean)^2.
+template <int L, int V, int K, bool MASK>
+__device__ __forceinline__ void row_moments(const float (&x)[V * K], const Part<L, V, K, MASK>& part, int d,
+                                            const NormArgs& n, RowShared<L>& shared, int turn, float& mean,
+                                            float& rstd) {
+  constexpr int E = V * K, W = L / 64;
+  const float inv = 1.0f / d;
+  float own_mean = 0.0f, sum = 0.0f, m2 = 0.0f;
+  const int wave = L > 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   if (!n.rms) {
-    float s = 0.0f;
-    for (int c = threadIdx.x; c < d; c += kThreads) s += load(c);
-    mean = block_sum_256(s, red) / d;
-  }
-  float s = 0.0f;
-  for (int c = threadIdx.x; c < d; c += kThreads) {
-    const float e = load(c) - mean;
-    s += e * e;
-  }
-  rstd = 1.0f / sqrtf(block_sum_256(s, red) / d + n.eps);
-}
-
-__device__ __forceinline__ float param(const float* p, int64_t i, float none) { return p ? p[i] : none; }
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) gated_norm_kernel(View o, View gate, View y, int H, int N, int d, NormArgs n) {
-  __shared__ float red[4];
-  const int64_t row = blockIdx.x;
-  const int t = static_cast<int>(row % N), h = static_cast<int>(row / N % H), b = static_cast<int>(row / N / H);
-  const T* op = reinterpret_cast<const T*>(o.data) + b * o.sb + h * o.sh + t * o.sn;
-  const T* gp = reinterpret_cast<const T*>(gate.data) + b * gate.sb + h * gate.sh + t * gate.sn;
-  T* yp = reinterpret_cast<T*>(y.data) + b * y.sb + h * y.sh + t * y.sn;
-  float mean, rstd;
-  row_stats([&](int c) { return Elem<T>::load(op, c); }, d, n, red, mean, rstd);
-  for (int c = threadIdx.x; c < d; c += kThreads) {
-    const int64_t i = static_cast<int64_t>(h) * d + c;
-    float z = fmaf((Elem<T>::load(op, c) - mean) * rstd, param(n.weight, i, 1.0f), param(n.bias, i, 0.0f));
-    if (gate.data) {
-      float s, less;
-      const float g = Elem<T>::load(gp, c);
-      sigmoid_pair(g, s, less);
-      z *= g * s;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += x[e];
+    sum = lanes_sum<(L < 64 ? L : 64)>(sum);
+    if constexpr (L > 64) {
+      const int own = Part<L, V, K, MASK>::count(wave, d);
+      own_mean = own > 0 ? sum / own : 0.0f;
+    } else {
+      own_mean = sum * inv;
     }
-    Elem<T>::store(yp, c, z);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float e = part.own(k, j) ? x[k * V + j] - own_mean : 0.0f;
+      m2 = fmaf(e, e, m2);
+    }
+  m2 = lanes_sum<(L < 64 ? L : 64)>(m2);
+  mean = own_mean;
+  if constexpr (L > 64) {
+    if ((threadIdx.x & 63) == 0) shared.moment[turn][wave] = make_float2(sum, m2);
+    lds_only_barrier();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += shared.moment[turn][w].x;
+    mean = n.rms ? 0.0f : sum * inv;
+    m2 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 m = shared.moment[turn][w];
+      m2 += m.y;
+      const int own = Part<L, V, K, MASK>::count(w, d);
+      if (!n.rms && own > 0) {
+        const float e = m.x / own - mean;
+        m2 = fmaf(own * e, e, m2);
+      }
+    }
+  }
+  rstd = 1.0f / sqrtf(fmaf(m2, inv, n.eps));
+}
+
+// Sums of a and b over the row.
+template <int L>
+__device__ __forceinline__ void row_sums(float& a, float& b, RowShared<L>& shared) {
+  a = lanes_sum<(L < 64 ? L : 64)>(a);
+  b = lanes_sum<(L < 64 ? L : 64)>(b);
+  if constexpr (L > 64) {
+    if ((threadIdx.x & 63) == 0) shared.sums[threadIdx.x >> 6] = make_float2(a, b);
+    lds_only_barrier();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < L / 64; ++w) {
+      a += shared.sums[w].x;
+      b += shared.sums[w].y;
+    }
   }
 }
 
-// Grid (parts, H): a workgroup takes every parts-th row of its head and adds
-// what its threads' columns contribute to its own rows of the partial sums.
+// The rows of a thread: row `first` of the batch's B * N, then every step-th.
+struct RowWalk {
+  int b, n, db, dn, N;
+  __device__ __forceinline__ RowWalk(int first, int step, int N) : N(N) {
+    b = first / N;
+    n = first - b * N;
+    db = step / N;
+    dn = step - db * N;
+  }
+  __device__ __forceinline__ void next() {
+    b += db;
+    n += dn;
+    if (n >= N) {
+      n -= N;
+      ++b;
+    }
+  }
+};
+
 template <typename T>
+__device__ __forceinline__ T* at(const View& v, int b, int h, int n) {
+  return reinterpret_cast<T*>(v.data) + b * v.sb + h * v.sh + n * v.sn;
+}
+
+// ---------------------------------------------------------------------------
+// Gated norm
+
+// Grid (parts, H), 256 / L rows of a head at a time.
+template <typename T, int L, int V, int K, bool MASK>
 __global__ void __launch_bounds__(kThreads)
-gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, int B, int H, int N, int d, NormArgs n,
-                           float* partial) {
-  __shared__ float red[4];
-  const int h = blockIdx.y, parts = gridDim.x;
-  float* sums = partial ? partial + (static_cast<int64_t>(h) * parts + blockIdx.x) * kGatedNormSums * d : nullptr;
-  if (sums)
-    for (int c = threadIdx.x; c < d; c += kThreads) sums[c] = sums[d + c] = 0.0f;
-  for (int64_t row = blockIdx.x; row < static_cast<int64_t>(B) * N; row += parts) {
-    const int t = static_cast<int>(row % N), b = static_cast<int>(row / N);
-    const T* dyp = reinterpret_cast<const T*>(dy.data) + b * dy.sb + h * dy.sh + t * dy.sn;
-    const T* op = reinterpret_cast<const T*>(o.data) + b * o.sb + h * o.sh + t * o.sn;
-    const T* gp = reinterpret_cast<const T*>(gate.data) + b * gate.sb + h * gate.sh + t * gate.sn;
-    T* dop = reinterpret_cast<T*>(d_o.data) + b * d_o.sb + h * d_o.sh + t * d_o.sn;
-    T* dgp = reinterpret_cast<T*>(d_gate.data) + b * d_gate.sb + h * d_gate.sh + t * d_gate.sn;
-    float mean, rstd;
-    row_stats([&](int c) { return Elem<T>::load(op, c); }, d, n, red, mean, rstd);
-    auto dz_of = [&](int c) {
-      float v = Elem<T>::load(dyp, c);
-      if (gate.data) {
-        float s, less;
-        const float g = Elem<T>::load(gp, c);
-        sigmoid_pair(g, s, less);
-        v *= g * s;
-      }
-      return v;
-    };
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = threadIdx.x; c < d; c += kThreads) {
-      const int64_t i = static_cast<int64_t>(h) * d + c;
-      const float xhat = (Elem<T>::load(op, c) - mean) * rstd;
-      const float dz = dz_of(c);
-      if (gate.data) {
-        float s, less;
-        const float g = Elem<T>::load(gp, c);
-        sigmoid_pair(g, s, less);
-        const float z = fmaf(xhat, param(n.weight, i, 1.0f), param(n.bias, i, 0.0f));
-        Elem<T>::store(dgp, c, Elem<T>::load(dyp, c) * z * (s * fmaf(g, less, 1.0f)));
-      }
-      if (sums) {
-        sums[c] += dz * xhat;
-        sums[d + c] += dz;
-      }
-      const float q = dz * param(n.weight, i, 1.0f);
-      s1 += q;
-      s2 += q * xhat;
+gated_norm_kernel(View o, View gate, View y, int rows, int N, int d, NormArgs n) {
+  constexpr int E = V * K, G = kThreads / L;
+  __shared__ RowShared<L> shared;
+  const int h = blockIdx.y, g = threadIdx.x / L;
+  const Part<L, V, K, MASK> part(threadIdx.x % L, d);
+  float w[E], b[E];
+  part.params(n.weight ? n.weight + static_cast<int64_t>(h) * d : nullptr, 1.0f, w);
+  part.params(n.bias ? n.bias + static_cast<int64_t>(h) * d : nullptr, 0.0f, b);
+  const int step = gridDim.x * G;
+  RowWalk row(blockIdx.x * G + g, step, N);
+  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next()) {
+    const bool live = base + g < rows;  // a group past the rows goes along on row 0
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    const auto ow = part.load(at<const T>(o, rb, h, rn));
+    auto gw = ow;
+    if (gate.data) gw = part.load(at<const T>(gate, rb, h, rn));
+    float x[E], gv[E], mean, rstd;
+    part.values(ow, x);
+    row_moments(x, part, d, n, shared, 0, mean, rstd);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf((x[e] - mean) * rstd, w[e], b[e]);
+    if (gate.data) {
+      part.values(gw, gv);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] *= swish(gv[e]);
     }
-    s1 = n.rms ? 0.0f : block_sum_256(s1, red) / d;
-    s2 = block_sum_256(s2, red) / d;
-    for (int c = threadIdx.x; c < d; c += kThreads) {
-      const int64_t i = static_cast<int64_t>(h) * d + c;
-      const float xhat = (Elem<T>::load(op, c) - mean) * rstd;
-      Elem<T>::store(dop, c, rstd * (dz_of(c) * param(n.weight, i, 1.0f) - s1 - xhat * s2));
+    if (live) part.store(at<T>(y, rb, h, rn), x);
+  }
+}
+
+// The workgroup's sums of SUMS parameters, from its G groups' registers, to
+// its row of the partial sums.
+template <int SUMS, int G, typename P>
+__device__ __forceinline__ void leave_sums(const P& part, const float (&sums)[SUMS][P::E], float* to, int d) {
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int s = 0; s < SUMS; ++s) part.put(to + static_cast<int64_t>(s) * d, sums[s]);
+  } else {
+    // One parameter at a time, to keep the LDS at 16 KiB.
+    constexpr int width = kThreads * P::E / G;
+    __shared__ float all[G][width];
+#pragma unroll
+    for (int s = 0; s < SUMS; ++s) {
+      __syncthreads();
+      part.put(all[threadIdx.x / (kThreads / G)], sums[s]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += kThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) v += all[g][c];
+        to[static_cast<int64_t>(s) * d + c] = v;
+      }
     }
   }
 }
 
-// out[k][head * d + c] = sum over parts of partial[head][part][k][c].
+template <typename T, int L, int V, int K, bool MASK>
+__global__ void __launch_bounds__(kThreads)
+gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, int rows, int N, int d, NormArgs n,
+                           float* partial) {
+  constexpr int E = V * K, G = kThreads / L;
+  typedef Part<L, V, K, MASK> P;
+  __shared__ RowShared<L> shared;
+  const int h = blockIdx.y, g = threadIdx.x / L;
+  const P part(threadIdx.x % L, d);
+  float w[E], b[E], sums[kGatedNormSums][E];
+  part.params(n.weight ? n.weight + static_cast<int64_t>(h) * d : nullptr, 1.0f, w);
+  part.params(n.bias ? n.bias + static_cast<int64_t>(h) * d : nullptr, 0.0f, b);
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[0][e] = sums[1][e] = 0.0f;
+  const float inv = 1.0f / d;
+  const int step = gridDim.x * G;
+  RowWalk row(blockIdx.x * G + g, step, N);
+  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next()) {
+    const bool live = base + g < rows;
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    const auto ow = part.load(at<const T>(o, rb, h, rn));
+    const auto dw = part.load(at<const T>(dy, rb, h, rn));
+    auto gw = ow;
+    if (gate.data) gw = part.load(at<const T>(gate, rb, h, rn));
+    float x[E], q[E], mean, rstd;
+    part.values(ow, x);
+    row_moments(x, part, d, n, shared, 0, mean, rstd);
+    part.values(dw, q);
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = (x[e] - mean) * rstd;
+    if (gate.data) {
+      float gv[E];
+      part.values(gw, gv);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float s, less;
+        sigmoid_pair(gv[e], s, less);
+        const float slope = s * fmaf(gv[e], less, 1.0f), z = fmaf(x[e], w[e], b[e]);
+        const float dyv = q[e];
+        q[e] = dyv * (gv[e] * s);
+        gv[e] = dyv * z * slope;
+      }
+      if (live) part.store(at<T>(d_gate, rb, h, rn), gv);
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {  // q is 0 for channels that are not the thread's own
+      sums[0][e] = fmaf(q[e], x[e], sums[0][e]);
+      sums[1][e] += q[e];
+      q[e] *= w[e];
+      s1 += q[e];
+      s2 = fmaf(q[e], x[e], s2);
+    }
+    row_sums<L>(s1, s2, shared);
+    s1 = n.rms ? 0.0f : s1 * inv;
+    s2 *= inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = rstd * (q[e] - s1 - x[e] * s2);
+    if (live) part.store(at<T>(d_o, rb, h, rn), q);
+  }
+  if (partial)
+    leave_sums<kGatedNormSums, G, P>(
+        part, sums, partial + (static_cast<int64_t>(h) * gridDim.x + blockIdx.x) * kGatedNormSums * d, d);
+}
+
+// out[k][head * d + c] = sum over parts of partial[head][part][k][c]: 16
+// columns to a workgroup, 16 threads a column, joined in a fixed order. Grid
+// (columns / 16, sums).
 __global__ void __launch_bounds__(kThreads)
 param_sum_kernel(const float* partial, int heads, int parts, int sums, int d, float* out0, float* out1, float* out2) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  __shared__ float all[16][17];
   const int k = blockIdx.y;
   float* out = k == 0 ? out0 : k == 1 ? out1 : out2;
-  if (!out || i >= static_cast<int64_t>(heads) * d) return;
-  const int64_t head = i / d;
-  const int c = static_cast<int>(i - head * d);
+  if (!out) return;
+  const int64_t n = static_cast<int64_t>(heads) * d;
+  const int col = threadIdx.x & 15, lot = threadIdx.x >> 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + col;
   float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += partial[((head * parts + p) * sums + k) * d + c];
-  out[i] = s;
+  if (i < n) {
+    const int64_t head = i / d;
+    const float* p = partial + ((head * parts) * sums + k) * d + (i - head * d);
+    const int64_t stride = static_cast<int64_t>(sums) * d;
+#pragma unroll 8
+    for (int q = lot; q < parts; q += 16) s += p[q * stride];
+  }
+  all[lot][col] = s;
+  __syncthreads();
+  if (lot == 0 && i < n) {
+    s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) s += all[q][col];
+    out[i] = s;
+  }
 }
 
 hipError_t sum_params(const float* partial, int heads, int parts, int sums, int d, float* out0, float* out1,
                       float* out2, hipStream_t stream) {
   const int64_t n = static_cast<int64_t>(heads) * d;
-  param_sum_kernel<<<dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads), sums), kThreads, 0, stream>>>(
-      partial, heads, parts, sums, d, out0, out1, out2);
+  param_sum_kernel<<<dim3(static_cast<unsigned>((n + 15) / 16), sums), kThreads, 0, stream>>>(partial, heads, parts,
+                                                                                             sums, d, out0, out1, out2);
   return hipGetLastError();
 }
 
-template <typename T, typename TR>
-__global__ void __launch_bounds__(kThreads)
-residual_norm_kernel(View x, View residual, View y, View r, int N, int D, NormArgs n, const float* scale, float alpha) {
-  __shared__ float red[4];
-  const int t = blockIdx.x % N, b = blockIdx.x / N;
-  const T* xp = reinterpret_cast<const T*>(x.data) + b * x.sb + t * x.sn;
-  const TR* sp = reinterpret_cast<const TR*>(residual.data) + b * residual.sb + t * residual.sn;
-  T* yp = reinterpret_cast<T*>(y.data) + b * y.sb + t * y.sn;
-  TR* rp = reinterpret_cast<TR*>(r.data) + b * r.sb + t * r.sn;
-  auto value = [&](int c) {
-    return fmaf(alpha, Elem<TR>::load(sp, c), param(scale, c, 1.0f) * Elem<T>::load(xp, c));
-  };
-  float mean, rstd;
-  row_stats(value, D, n, red, mean, rstd);
-  for (int c = threadIdx.x; c < D; c += kThreads) {
-    const float v = value(c);
-    Elem<TR>::store(rp, c, v);
-    Elem<T>::store(yp, c, fmaf((v - mean) * rstd, param(n.weight, c, 1.0f), param(n.bias, c, 0.0f)));
+// ---------------------------------------------------------------------------
+// Residual norm: a workgroup of max(256, L) threads, 256 / L rows at a time.
+
+constexpr int threads_of(int L) { return L > kThreads ? L : kThreads; }
+
+template <typename T, typename TR, int L, int V, int K, bool MASK>
+__global__ void __launch_bounds__(threads_of(L))
+residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int D, NormArgs n, const float* scale,
+                     float alpha) {
+  constexpr int E = V * K, G = threads_of(L) / L;
+  __shared__ RowShared<L> shared;
+  const int g = threadIdx.x / L;
+  const Part<L, V, K, MASK> part(threadIdx.x % L, D);
+  const int step = gridDim.x * G;
+  RowWalk row(blockIdx.x * G + g, step, N);
+  int turn = 0;
+  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next(), turn ^= 1) {
+    const bool live = base + g < rows;
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    const auto rw = part.load(at<const TR>(residual, rb, 0, rn));
+    const auto xw = part.load(at<const T>(x, rb, 0, rn));
+    float v[E], p[E], mean, rstd;
+    part.values(xw, v);
+    if (scale) {
+      part.params(scale, 1.0f, p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= p[e];
+    }
+    part.values(rw, p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = fmaf(alpha, p[e], v[e]);
+    if (live) part.store(at<TR>(r, rb, 0, rn), v);
+    row_moments(v, part, D, n, shared, turn, mean, rstd);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (v[e] - mean) * rstd;
+    if (n.weight) {
+      part.params(n.weight, 1.0f, p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= p[e];
+    }
+    if (n.bias) {
+      part.params(n.bias, 0.0f, p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += p[e];
+    }
+    if (live) part.store(at<T>(y, rb, 0, rn), v);
   }
 }
 
-template <typename T, typename TR>
-__global__ void __launch_bounds__(kThreads)
-residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dres, int64_t rows, int N, int D,
-                              NormArgs n, const float* scale, float alpha, float* partial) {
-  __shared__ float red[4];
-  float* sums = partial ? partial + static_cast<int64_t>(blockIdx.x) * kResidualNormSums * D : nullptr;
-  if (sums)
-    for (int c = threadIdx.x; c < kResidualNormSums * D; c += kThreads) sums[c] = 0.0f;
-  __syncthreads();
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int t = static_cast<int>(row % N), b = static_cast<int>(row / N);
-    const T* dyp = reinterpret_cast<const T*>(dy.data) + b * dy.sb + t * dy.sn;
-    const TR* drp = dr.data ? reinterpret_cast<const TR*>(dr.data) + b * dr.sb + t * dr.sn : nullptr;
-    const TR* rp = reinterpret_cast<const TR*>(r.data) + b * r.sb + t * r.sn;
-    const T* xp = x.data ? reinterpret_cast<const T*>(x.data) + b * x.sb + t * x.sn : nullptr;
-    T* dxp = dx.data ? reinterpret_cast<T*>(dx.data) + b * dx.sb + t * dx.sn : nullptr;
-    TR* dsp = reinterpret_cast<TR*>(dres.data) + b * dres.sb + t * dres.sn;
-    float mean, rstd;
-    row_stats([&](int c) { return Elem<TR>::load(rp, c); }, D, n, red, mean, rstd);
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = threadIdx.x; c < D; c += kThreads) {
-      const float q = Elem<T>::load(dyp, c) * param(n.weight, c, 1.0f);
-      s1 += q;
-      s2 += q * ((Elem<TR>::load(rp, c) - mean) * rstd);
+template <typename T, typename TR, int L, int V, int K, bool MASK>
+__global__ void __launch_bounds__(threads_of(L))
+residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dres, int rows, int N, int D, NormArgs n,
+                              const float* scale, float alpha, float* partial) {
+  constexpr int E = V * K, G = threads_of(L) / L;
+  typedef Part<L, V, K, MASK> P;
+  __shared__ RowShared<L> shared;
+  const int g = threadIdx.x / L;
+  const P part(threadIdx.x % L, D);
+  const float inv = 1.0f / D;
+  float sums[kResidualNormSums][E];
+#pragma unroll
+  for (int s = 0; s < kResidualNormSums; ++s)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[s][e] = 0.0f;
+  const int step = gridDim.x * G;
+  RowWalk row(blockIdx.x * G + g, step, N);
+  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next()) {
+    const bool live = base + g < rows;
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    const auto vw = part.load(at<const TR>(r, rb, 0, rn));
+    const auto gw = part.load(at<const T>(dy, rb, 0, rn));
+    auto sw = vw;
+    if (dr.data) sw = part.load(at<const TR>(dr, rb, 0, rn));
+    auto xw = gw;
+    if (x.data) xw = part.load(at<const T>(x, rb, 0, rn));
+    float v[E], q[E], p[E], mean, rstd;
+    part.values(vw, v);
+    row_moments(v, part, D, n, shared, 0, mean, rstd);
+    part.values(gw, q);
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = 0.0f;
     }
-    s1 = n.rms ? 0.0f : block_sum_256(s1, red) / D;
-    s2 = block_sum_256(s2, red) / D;
-    for (int c = threadIdx.x; c < D; c += kThreads) {
-      const float g = Elem<T>::load(dyp, c);
-      const float xhat = (Elem<TR>::load(rp, c) - mean) * rstd;
-      const float v = (drp ? Elem<TR>::load(drp, c) : 0.0f) +
-                      rstd * (g * param(n.weight, c, 1.0f) - s1 - xhat * s2);
-      if (sums) {
-        if (xp) sums[c] += v * Elem<T>::load(xp, c);
-        sums[D + c] += g * xhat;
-        sums[2 * D + c] += g;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (v[e] - mean) * rstd;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {  // q is 0 for channels that are not the thread's own
+      sums[1][e] = fmaf(q[e], v[e], sums[1][e]);
+      sums[2][e] += q[e];
+    }
+    if (n.weight) {
+      part.params(n.weight, 1.0f, p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] *= p[e];
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      s1 += q[e];
+      s2 = fmaf(q[e], v[e], s2);
+    }
+    row_sums<L>(s1, s2, shared);
+    s1 = n.rms ? 0.0f : s1 * inv;
+    s2 *= inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = rstd * (q[e] - s1 - v[e] * s2);
+    if (dr.data) {
+      part.values(sw, p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] += p[e];
+    }
+    if (x.data) {
+      part.values(xw, p);  // 0 for channels that are not the thread's own
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[0][e] = live ? fmaf(q[e], p[e], sums[0][e]) : sums[0][e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = alpha * q[e];
+    if (live) part.store(at<TR>(dres, rb, 0, rn), v);
+    if (dx.data) {
+      if (scale) {
+        part.params(scale, 1.0f, p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[e] *= p[e];
       }
-      Elem<TR>::store(dsp, c, alpha * v);
-      if (dxp) Elem<T>::store(dxp, c, param(scale, c, 1.0f) * v);
+      if (live) part.store(at<T>(dx, rb, 0, rn), q);
     }
   }
+  if (partial)
+    leave_sums<kResidualNormSums, G, P>(part, sums,
+                                        partial + static_cast<int64_t>(blockIdx.x) * kResidualNormSums * D, D);
+}
+
+// ---------------------------------------------------------------------------
+// Which instance takes a width: the fewest lanes that hold it at 16 values
+// each (8 of bf16 or 4 of fp32 to an access), one value a lane for rows
+// shorter than an access.
+
+#define RET_ROW(kernel, L, V, K, ...)                                                \
+  do {                                                                               \
+    if (d == L * V * K) kernel(L, V, K, false, __VA_ARGS__);                         \
+    else kernel(L, V, K, true, __VA_ARGS__);                                         \
+    return hipGetLastError();                                                        \
+  } while (0)
+
+#define RET_HEAD_ROWS(kernel, V, ...)                                                \
+  do {                                                                               \
+    if (d < V) RET_ROW(kernel, 8, 1, 1, __VA_ARGS__);                                \
+    if (d <= 8 * V) RET_ROW(kernel, 8, V, 1, __VA_ARGS__);                           \
+    if (d <= 16 * V) RET_ROW(kernel, 16, V, 1, __VA_ARGS__);                         \
+    if (d <= 32 * V) RET_ROW(kernel, 32, V, 1, __VA_ARGS__);                         \
+    if (d <= 64 * V) RET_ROW(kernel, 64, V, 1, __VA_ARGS__);                         \
+    if (V < 8 && d <= 128 * V) RET_ROW(kernel, 64, V, (V < 8 ? 2 : 1), __VA_ARGS__); \
+    RET_ROW(kernel, 64, V, 16 / V, __VA_ARGS__);                                     \
+  } while (0)
+
+#define RET_MODEL_ROWS(kernel, V, ...)                                               \
+  do {                                                                               \
+    if (d < V) RET_ROW(kernel, 64, 1, 1, __VA_ARGS__);                               \
+    if (d <= 64 * V) RET_ROW(kernel, 64, V, 1, __VA_ARGS__);                         \
+    if (d <= 1024) RET_ROW(kernel, 64, V, 16 / V, __VA_ARGS__);                      \
+    if (d <= 2048) RET_ROW(kernel, 256, V, 8 / V, __VA_ARGS__);                      \
+    if (d <= 4096) RET_ROW(kernel, 256, V, 16 / V, __VA_ARGS__);                     \
+    if (d <= 8192) RET_ROW(kernel, 512, V, 16 / V, __VA_ARGS__);                     \
+    RET_ROW(kernel, 1024, V, 16 / V, __VA_ARGS__);                                   \
+  } while (0)
+
+// Rows that a workgroup of a launch over rows of d values takes at a time.
+int rows_at_once(int d, int dtype, bool heads) {
+  const int V = dtype == 0 ? 4 : 8;
+  int L = 64;
+  if (heads) {
+    L = d < V ? 8 : d <= 8 * V ? 8 : d <= 16 * V ? 16 : d <= 32 * V ? 32 : 64;
+  } else if (d > 1024) {
+    return 1;
+  }
+  return kThreads / L;
 }
 
 }  // namespace
 
 hipError_t launch_gated_norm(int dtype, const View& o, const View& gate, const View& y, int B, int H, int N, int d,
                              const NormArgs& norm, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(B) * H * N));
-  if (dtype == 0) gated_norm_kernel<float><<<grid, kThreads, 0, stream>>>(o, gate, y, H, N, d, norm);
-  else gated_norm_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(o, gate, y, H, N, d, norm);
-  return hipGetLastError();
+  const int rows = B * N;
+  const dim3 grid(norm_parts(H, rows, rows_at_once(d, dtype, true), kForwardGroups), H);
+#define RET_LAUNCH(L, V, K, MASK, T) \
+  gated_norm_kernel<T, L, V, K, MASK><<<grid, kThreads, 0, stream>>>(o, gate, y, rows, N, d, norm)
+  if (dtype == 0) RET_HEAD_ROWS(RET_LAUNCH, 4, float);
+  RET_HEAD_ROWS(RET_LAUNCH, 8, uint16_t);
+#undef RET_LAUNCH
 }
+
+namespace {
+
+hipError_t gated_norm_backward(int dtype, const View& dy, const View& o, const View& gate, const View& d_o,
+                               const View& d_gate, int parts, int H, int rows, int N, int d, const NormArgs& norm,
+                               float* partial, hipStream_t stream) {
+  const dim3 grid(parts, H);
+#define RET_LAUNCH(L, V, K, MASK, T)                                                                             \
+  gated_norm_backward_kernel<T, L, V, K, MASK><<<grid, kThreads, 0, stream>>>(dy, o, gate, d_o, d_gate, rows, N, \
+                                                                              d, norm, partial)
+  if (dtype == 0) RET_HEAD_ROWS(RET_LAUNCH, 4, float);
+  RET_HEAD_ROWS(RET_LAUNCH, 8, uint16_t);
+#undef RET_LAUNCH
+}
+
+hipError_t residual_norm_backward(int dtype, int stream_dtype, const View& dy, const View& dr, const View& r,
+                                  const View& x, const View& dx, const View& dres, int parts, int rows, int N, int d,
+                                  const NormArgs& norm, const float* scale, float alpha, float* partial,
+                                  hipStream_t stream) {
+#define RET_LAUNCH(L, V, K, MASK, T, TR)                                                              \
+  residual_norm_backward_kernel<T, TR, L, V, K, MASK><<<parts, threads_of(L), 0, stream>>>(           \
+      dy, dr, r, x, dx, dres, rows, N, d, norm, scale, alpha, partial)
+  if (dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 4, float, float);
+  if (stream_dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, float);
+  RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, uint16_t);
+#undef RET_LAUNCH
+}
+
+}  // namespace
 
 hipError_t launch_gated_norm_backward(int dtype, const View& grad_y, const View& o, const View& gate,
                                       const View& grad_o, const View& grad_gate, int B, int H, int N, int d,
                                       const NormArgs& norm, float* grad_weight, float* grad_bias, void* workspace,
                                       hipStream_t stream) {
-  const ParamPlan p = plan_params(H, static_cast<int64_t>(B) * N, d, kGatedNormSums);
+  const int rows = B * N, parts = norm_parts(H, rows, rows_at_once(d, dtype, true), kBackwardGroups);
   float* partial = grad_weight || grad_bias ? static_cast<float*>(workspace) : nullptr;
-  const dim3 grid(p.parts, H);
-  if (dtype == 0)
-    gated_norm_backward_kernel<float><<<grid, kThreads, 0, stream>>>(grad_y, o, gate, grad_o, grad_gate, B, H, N, d,
-                                                                     norm, partial);
-  else
-    gated_norm_backward_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(grad_y, o, gate, grad_o, grad_gate, B, H, N,
-                                                                        d, norm, partial);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e =
+      gated_norm_backward(dtype, grad_y, o, gate, grad_o, grad_gate, parts, H, rows, N, d, norm, partial, stream);
   if (e != hipSuccess || !partial) return e;
-  return sum_params(partial, H, p.parts, kGatedNormSums, d, grad_weight, grad_bias, nullptr, stream);
+  return sum_params(partial, H, parts, kGatedNormSums, d, grad_weight, grad_bias, nullptr, stream);
 }
 
 hipError_t launch_residual_norm(int dtype, int stream_dtype, const View& x, const View& residual, const View& y,
-                                const View& r, int B, int N, int D, const NormArgs& norm, const float* scale,
+                                const View& r, int B, int N, int d, const NormArgs& norm, const float* scale,
                                 float alpha, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(B) * N));
-  if (dtype == 0)
-    residual_norm_kernel<float, float><<<grid, kThreads, 0, stream>>>(x, residual, y, r, N, D, norm, scale, alpha);
-  else if (stream_dtype == 0)
-    residual_norm_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(x, residual, y, r, N, D, norm, scale, alpha);
-  else
-    residual_norm_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(x, residual, y, r, N, D, norm, scale,
-                                                                            alpha);
-  return hipGetLastError();
+  const int rows = B * N, parts = norm_parts(1, rows, rows_at_once(d, dtype, false), kForwardGroups);
+#define RET_LAUNCH(L, V, K, MASK, T, TR)                                                                          \
+  residual_norm_kernel<T, TR, L, V, K, MASK><<<parts, threads_of(L), 0, stream>>>(x, residual, y, r, rows, N, d, \
+                                                                                  norm, scale, alpha)
+  if (dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 4, float, float);
+  if (stream_dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, float);
+  RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, uint16_t);
+#undef RET_LAUNCH
 }
 
 hipError_t launch_residual_norm_backward(int dtype, int stream_dtype, const View& grad_y, const View& grad_r,
                                          const View& r, const View& x, const View& grad_x, const View& grad_residual,
-                                         int B, int N, int D, const NormArgs& norm, const float* scale, float alpha,
+                                         int B, int N, int d, const NormArgs& norm, const float* scale, float alpha,
                                          float* grad_scale, float* grad_weight, float* grad_bias, void* workspace,
                                          hipStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(B) * N;
-  const ParamPlan p = plan_params(1, rows, D, kResidualNormSums);
+  const int rows = B * N, parts = norm_parts(1, rows, rows_at_once(d, dtype, false), kBackwardGroups);
   float* partial = grad_scale || grad_weight || grad_bias ? static_cast<float*>(workspace) : nullptr;
   View xs = x;
   if (!grad_scale) xs.data = nullptr;
-  const dim3 grid(p.parts);
-  if (dtype == 0)
-    residual_norm_backward_kernel<float, float><<<grid, kThreads, 0, stream>>>(
-        grad_y, grad_r, r, xs, grad_x, grad_residual, rows, N, D, norm, scale, alpha, partial);
-  else if (stream_dtype == 0)
-    residual_norm_backward_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(
-        grad_y, grad_r, r, xs, grad_x, grad_residual, rows, N, D, norm, scale, alpha, partial);
-  else
-    residual_norm_backward_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(
-        grad_y, grad_r, r, xs, grad_x, grad_residual, rows, N, D, norm, scale, alpha, partial);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = residual_norm_backward(dtype, stream_dtype, grad_y, grad_r, r, xs, grad_x, grad_residual, parts,
+                                              rows, N, d, norm, scale, alpha, partial, stream);
   if (e != hipSuccess || !partial) return e;
-  return sum_params(partial, 1, p.parts, kResidualNormSums, D, grad_scale, grad_weight, grad_bias, stream);
+  return sum_params(partial, 1, parts, kResidualNormSums, d, grad_scale, grad_weight, grad_bias, stream);
 }
 
 }  // namespace ret
