@@ -160,20 +160,23 @@ int retention_residual_norm(const retention_view_t* x, const retention_view_t* r
 
 /*
  * Gradients of retention_residual_norm for grad_y = dL/dy and grad_r = dL/dr
- * (NULL: 0). r is the forward call's output. With t = grad_r + (the norm's
- * gradient for grad_y * weight):
+ * (NULL: 0). With t = grad_r + (the norm's gradient for grad_y * weight):
  *   grad_residual = alpha * t (stream_dtype), grad_x = scale * t (dtype),
  *   grad_scale = sum over rows of x * t, grad_weight = sum of grad_y * norm(r),
  *   grad_bias = sum of grad_y   (fp32 [D], each NULL: not wanted)
- * grad_x may be NULL (not wanted, or equal to grad_residual); x is read for
- * grad_scale only and may be NULL otherwise.
+ * The row that was normed is read from r, the forward call's output, with the
+ * rounding it has in the stream's type; with residual (and x) given it is
+ * formed again from them instead, and r is not read and may be NULL: with a
+ * bf16 stream grad_weight then carries fp32 accuracy. grad_x may be NULL (not
+ * wanted, or equal to grad_residual); x is read for grad_scale or with
+ * residual only and may be NULL otherwise.
  */
 size_t retention_residual_norm_backward_workspace_bytes(int B, int N, int D, int dtype, int with_params);
 
 int retention_residual_norm_backward(const retention_view_t* grad_y, const retention_view_t* grad_r,
                                      const retention_view_t* r, const retention_view_t* x,
-                                     const retention_view_t* grad_x, const retention_view_t* grad_residual, int B,
-                                     int N, int D, int dtype, int stream_dtype, const retention_norm_t* norm,
+                                     const retention_view_t* residual, const retention_view_t* grad_x,
+                                     const retention_view_t* grad_residual, int B, int N, int D, int dtype, int stream_dtype, const retention_norm_t* norm,
                                      const float* scale, float alpha, float* grad_scale, float* grad_weight,
                                      float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
 

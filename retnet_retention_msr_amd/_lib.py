@@ -155,7 +155,7 @@ def declare_block(lib):
     lib.retention_residual_norm.restype = i
     lib.retention_residual_norm_backward_workspace_bytes.argtypes = [i] * 5
     lib.retention_residual_norm_backward_workspace_bytes.restype = size
-    lib.retention_residual_norm_backward.argtypes = [view] * 6 + [i] * 5 + [norm, vp, f, vp, vp, vp] + workspace
+    lib.retention_residual_norm_backward.argtypes = [view] * 7 + [i] * 5 + [norm, vp, f, vp, vp, vp] + workspace
     lib.retention_residual_norm_backward.restype = i
     return lib
 

@@ -24,7 +24,8 @@ from typing import Optional, Union
 
 import torch
 
-from . import GroupNorm, RetentionError, _dtype_code, _lib, _require, _require_workspace, _stream
+from . import GroupNorm, RetentionError, _dtype_code, _lib, _require, _require_workspace
+from . import _stream as _stream_of
 
 FORMS = {"sigmoid": 0, "log": 1}
 
@@ -41,6 +42,14 @@ class Norm:
 
 
 NormLike = Union[Norm, GroupNorm]
+
+# torch's current stream as a number, without building a Stream object (2 us a
+# call, a fifth of a decode step's whole host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t):
+    return _stream_of(t) if _raw_stream is None else _raw_stream(t.device.index)
 
 
 def _activations(t, name, dims):
@@ -75,7 +84,7 @@ def _same(t, name, like, dtype=None):
 
 
 def _new(like, dtype=None):
-    return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
+    return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _output(t, name, like, dtype=None):
@@ -406,19 +415,25 @@ def residual_norm_backward_workspace_bytes(B, N, D, dtype=torch.bfloat16, with_p
 
 
 def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale=None, alpha: float = 1.0,
-                           grads=None, workspace=None):
-    """Gradients of residual_norm for dL/dy = grad_y and dL/dr = grad_r (None = 0), r being the forward's output.
+                           residual=None, grads=None, workspace=None):
+    """Gradients of residual_norm for dL/dy = grad_y and dL/dr = grad_r (None = 0).
 
     Returns (grad_x, grad_residual, grad_scale, grad_weight, grad_bias):
     grad_scale (fp32 [D]) is formed when ``x`` and ``scale`` are given, the
-    norm's gradients where it has a weight or bias. Without a scale, with
-    alpha 1 and one dtype, the two activation gradients are equal and grad_x
-    is grad_residual, the same tensor. ``grads``: optional preallocated
-    (grad_x, grad_residual), two tensors.
+    norm's gradients where it has a weight or bias. ``r`` is the forward call's
+    output. In a bf16 stream it carries bf16's rounding, which grad_weight and
+    grad_scale then show; with ``residual`` and ``x`` given the row is formed
+    again from them in fp32 and r is not read (it may be None). Without a
+    scale, with alpha 1 and one dtype, the two activation gradients are equal
+    and grad_x is grad_residual, the same tensor. ``grads``: optional
+    preallocated (grad_x, grad_residual), two tensors.
     """
     _rows(grad_y, "grad_y")
     dt, dev, D = _dtype_code(grad_y), grad_y.device, grad_y.size(-1)
-    stream = _stream_dtype(r, "r", grad_y.dtype)
+    if residual is not None and x is None:
+        raise ValueError("residual needs x")
+    row, name = (r, "r") if residual is None else (residual, "residual")
+    stream = _stream_dtype(row, name, grad_y.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
         _require(scale, "scale", (D,), torch.float32, dev)
@@ -431,9 +446,9 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
         if len(grads) != 2:
             raise ValueError("grads must be (grad_x, grad_residual)")
     _same(grads[0], "grad_x", grad_y)
-    for name, t in (("r", r), ("grad_r", grad_r), ("grad_residual", grads[1])):
+    for what, t in ((name, row), ("grad_r", grad_r), ("grad_residual", grads[1])):
         if t is not None:
-            _rows_layout(_same(t, name, grad_y, stream), name)
+            _rows_layout(_same(t, what, grad_y, stream), what)
     if x is not None:
         _rows_layout(_same(x, "x", grad_y), "x")
     _rows_layout(grads[0], "grad_x")
@@ -444,8 +459,10 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     dims = _row_dims(grad_y)
     nbytes = int(_lib.load().retention_residual_norm_backward_workspace_bytes(*dims, dt, int(params)))
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_residual_norm_backward", dev, _row_view(grad_y), _row_view(grad_r), _row_view(r),
-          _row_view(x if d_scale is not None else None), None if shared else _row_view(grads[0]), _row_view(grads[1]),
-          *dims, dt, _lib.RET_F32 if stream == torch.float32 else dt, n, _ptr(scale), float(alpha), _ptr(d_scale),
-          _ptr(dw), _ptr(db), _ptr(workspace), have, _stream(grad_y))
+    _call("retention_residual_norm_backward", dev, _row_view(grad_y), _row_view(grad_r),
+          None if residual is not None else _row_view(r),
+          _row_view(x if d_scale is not None or residual is not None else None), _row_view(residual),
+          None if shared else _row_view(grads[0]), _row_view(grads[1]), *dims, dt,
+          _lib.RET_F32 if stream == torch.float32 else dt, n, _ptr(scale), float(alpha), _ptr(d_scale), _ptr(dw),
+          _ptr(db), _ptr(workspace), have, _stream(grad_y))
     return grads[0], grads[1], d_scale, dw, db

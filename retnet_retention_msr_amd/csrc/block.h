@@ -95,15 +95,27 @@ hipError_t launch_gated_norm(int dtype, const View& o, const View& gate, const V
                              const NormArgs& norm, hipStream_t stream);
 // Workgroups of a norm's launch, per head: as many as the rows give at
 // `at_once` rows each, at most `groups` over all heads.
-constexpr int kForwardGroups = 4096, kBackwardGroups = 1024;
+constexpr int kForwardGroups = 4096;
 inline int norm_parts(int heads, int rows, int at_once, int groups) {
   const int want = (rows - 1) / at_once + 1, most = (groups + heads - 1) / heads;
   return want < most ? want : most;
 }
+// A workgroup of the backward should go over enough rows that its partial sums
+// do not count: 8 turns at least, and 512 workgroups at least. Up to 4096
+// where there are rows enough: the workgroups at work then lie in fewer heads.
+constexpr int kGatedBackGroups = 4096;
+inline int gated_back_groups(int heads, int rows, int at_once) {
+  const int64_t turns = static_cast<int64_t>(heads) * ((rows - 1) / at_once + 1) / 8;
+  return turns < 512 ? 512 : turns < kGatedBackGroups ? static_cast<int>(turns) : kGatedBackGroups;
+}
+// As many workgroups as are at work at once: four of 256 threads to a CU, two
+// of 512.
+constexpr int kResidualBackGroups = 1024;
+inline int residual_back_groups(int d) { return d <= 2048 ? kResidualBackGroups : kResidualBackGroups / 2; }
 // Bytes of the backward's partial sums: a row of `sums` times d floats for
 // each of its workgroups (whatever the rows a workgroup takes at a time).
-inline size_t param_bytes(int heads, int rows, int d, int sums) {
-  return static_cast<size_t>(heads) * norm_parts(heads, rows, 1, kBackwardGroups) * sums * d * sizeof(float);
+inline size_t param_bytes(int heads, int rows, int d, int sums, int groups) {
+  return static_cast<size_t>(heads) * norm_parts(heads, rows, 1, groups) * sums * d * sizeof(float);
 }
 constexpr int kGatedNormSums = 2;     // weight, bias
 constexpr int kResidualNormSums = 3;  // scale, weight, bias
@@ -114,10 +126,11 @@ hipError_t launch_gated_norm_backward(int dtype, const View& grad_y, const View&
 hipError_t launch_residual_norm(int dtype, int stream_dtype, const View& x, const View& residual, const View& y,
                                 const View& r, int B, int N, int D, const NormArgs& norm, const float* scale,
                                 float alpha, hipStream_t stream);
-// grad_r.data, x.data and grad_x.data may be nullptr.
+// grad_r.data, x.data and grad_x.data may be nullptr; with residual.data the
+// row is formed from residual and x and r.data may be nullptr.
 hipError_t launch_residual_norm_backward(int dtype, int stream_dtype, const View& grad_y, const View& grad_r,
-                                         const View& r, const View& x, const View& grad_x, const View& grad_residual,
-                                         int B, int N, int D, const NormArgs& norm, const float* scale, float alpha,
+                                         const View& r, const View& x, const View& residual, const View& grad_x,
+                                         const View& grad_residual, int B, int N, int D, const NormArgs& norm, const float* scale, float alpha,
                                          float* grad_scale, float* grad_weight, float* grad_bias, void* workspace,
                                          hipStream_t stream);
 

@@ -301,7 +301,7 @@ int retention_gated_norm(const retention_view_t* o, const retention_view_t* gate
 
 size_t retention_gated_norm_backward_workspace_bytes(int B, int H, int N, int d, int dtype, int with_params) {
   if (check_dims(B, H, N, d, dtype) != RET_OK || d > RETENTION_MAX_DV || H > RETENTION_MAX_HEADS || !with_params) return 0;
-  return ret::param_bytes(H, B * N, d, ret::kGatedNormSums);
+  return ret::param_bytes(H, B * N, d, ret::kGatedNormSums, ret::kGatedBackGroups);
 }
 
 int retention_gated_norm_backward(const retention_view_t* grad_y, const retention_view_t* o,
@@ -334,7 +334,7 @@ int retention_gated_norm_backward(const retention_view_t* grad_y, const retentio
     ranges.output(r);
   }
   if (grad_weight || grad_bias) {
-    const size_t need = ret::param_bytes(H, B * N, d, ret::kGatedNormSums);
+    const size_t need = ret::param_bytes(H, B * N, d, ret::kGatedNormSums, ret::kGatedBackGroups);
     if (!workspace || workspace_bytes < need || misaligned(workspace, 4)) return RET_ERR_INVALID_ARG;
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }
@@ -373,12 +373,13 @@ int retention_residual_norm(const retention_view_t* x, const retention_view_t* r
 
 size_t retention_residual_norm_backward_workspace_bytes(int B, int N, int D, int dtype, int with_params) {
   if (check_dims(B, 1, N, D, dtype) != RET_OK || D > RETENTION_MAX_MODEL_DIM || !with_params) return 0;
-  return ret::param_bytes(1, B * N, D, ret::kResidualNormSums);
+  return ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::kResidualBackGroups);
 }
 
 int retention_residual_norm_backward(const retention_view_t* grad_y, const retention_view_t* grad_r,
                                      const retention_view_t* r, const retention_view_t* x,
-                                     const retention_view_t* grad_x, const retention_view_t* grad_residual, int B,
+                                     const retention_view_t* residual, const retention_view_t* grad_x,
+                                     const retention_view_t* grad_residual, int B,
                                      int N, int D, int dtype, int stream_dtype, const retention_norm_t* norm,
                                      const float* scale, float alpha, float* grad_scale, float* grad_weight,
                                      float* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
@@ -390,15 +391,17 @@ int retention_residual_norm_backward(const retention_view_t* grad_y, const reten
   Ranges ranges;
   NormArgs n;
   if ((st = check_norm(norm, D, &n, &ranges)) != RET_OK) return st;
-  View vdy, vdr, vr, vx, vdx, vdres;
+  View vdy, vdr, vr, vx, vres, vdx, vdres;
   Range g;
   if ((st = check_view(grad_y, B, 1, N, D, dtype, true, false, &vdy, &g)) != RET_OK) return st;
   ranges.input(g);
   if ((st = check_view(grad_r, B, 1, N, D, stream_dtype, false, false, &vdr, &g)) != RET_OK) return st;
   ranges.input(g);
-  if ((st = check_view(r, B, 1, N, D, stream_dtype, true, false, &vr, &g)) != RET_OK) return st;
+  if ((st = check_view(residual, B, 1, N, D, stream_dtype, false, false, &vres, &g)) != RET_OK) return st;
   ranges.input(g);
-  if ((st = check_view(x, B, 1, N, D, dtype, grad_scale != nullptr, false, &vx, &g)) != RET_OK) return st;
+  if ((st = check_view(r, B, 1, N, D, stream_dtype, !vres.data, false, &vr, &g)) != RET_OK) return st;
+  ranges.input(g);
+  if ((st = check_view(x, B, 1, N, D, dtype, grad_scale || vres.data, false, &vx, &g)) != RET_OK) return st;
   ranges.input(g);
   if ((st = check_view(grad_x, B, 1, N, D, dtype, false, true, &vdx, &g)) != RET_OK) return st;
   ranges.output(g);
@@ -411,12 +414,12 @@ int retention_residual_norm_backward(const retention_view_t* grad_y, const reten
     ranges.output(g);
   }
   if (grad_scale || grad_weight || grad_bias) {
-    const size_t need = ret::param_bytes(1, B * N, D, ret::kResidualNormSums);
+    const size_t need = ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::kResidualBackGroups);
     if (!workspace || workspace_bytes < need || misaligned(workspace, 4)) return RET_ERR_INVALID_ARG;
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }
   if (ranges.clash()) return RET_ERR_INVALID_ARG;
-  return status_of(ret::launch_residual_norm_backward(dtype, stream_dtype, vdy, vdr, vr, vx, vdx, vdres, B, N, D, n,
+  return status_of(ret::launch_residual_norm_backward(dtype, stream_dtype, vdy, vdr, vr, vx, vres, vdx, vdres, B, N, D, n,
                                                       scale, alpha, grad_scale, grad_weight, grad_bias, workspace,
                                                       static_cast<hipStream_t>(stream)));
 }

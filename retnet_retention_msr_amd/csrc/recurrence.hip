@@ -37,7 +37,6 @@ namespace ret {
 
 namespace {
 
-constexpr int kThreads = 64;
 constexpr uint32_t kXcds = 8;
 
 struct Piece {
@@ -550,50 +549,96 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   }
 }
 
-// Grid: x over the channels of a row (H * d), y-strided over the B rows. A
-// block takes row b unless an earlier row names the same slot; then it goes on
-// with the later rows of that slot.
-template <typename T, int FORM>
-__global__ void __launch_bounds__(kThreads)
+// ---------------------------------------------------------------------------
+// One token
+
+constexpr int kStepThreads = 256;
+
+// Grid: x over the pieces of V channels of a row's H heads, y over the B rows
+// (strided). A thread takes V channels of a head; the last piece of a head is
+// moved back to end with it, its first `shift` channels left to the neighbour.
+// With slots a block first looks through them, its loads already on their
+// way: a row whose slot an earlier row names is left to that row's block,
+// which goes on with the later rows of its slot in order. Bound by HBM for
+// large batches (three elements and an fp32 state read and written per
+// channel), by the launch below a few megabytes.
+template <typename T, int FORM, int V>
+__global__ void __launch_bounds__(kStepThreads)
 step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int nstates, const int* slots) {
-  const int channels = H * d;
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= channels) return;
-  const int h = c / d, j = c - h * d;
+  __shared__ int named[kStepThreads / 64];
+  typedef Pack<T, V> P;
+  const int pieces = (d + V - 1) / V;
+  const int piece = blockIdx.x * kStepThreads + threadIdx.x;
+  const bool in = piece < pieces * H;
+  const int h = in ? piece / pieces : 0;
+  const int c = in ? (piece - h * pieces) * V : 0;
+  const int start = c < d - V ? c : d - V, shift = c - start;
   for (int b = blockIdx.y; b < B; b += gridDim.y) {
-    int slot = b;
+    const int slot = slots ? slots[b] : b;
+    if (slot < 0 || slot >= nstates) continue;
+    float* state = states + (static_cast<int64_t>(slot) * H + h) * d + start;
+    float now[V];
+    Pack<float, V>::unpack(Pack<float, V>::load(state), now);
+    auto gw = P::load(row_of<T>(gate, b, h) + start);
+    auto xw = P::load(row_of<T>(x, b, h) + start);
+    bool later = false;
     if (slots) {
-      slot = slots[b];
-      if (slot < 0 || slot >= nstates) continue;
-      bool later = false;
-      for (int i = 0; i < b; ++i) later |= slots[i] == slot;
-      if (later) continue;
+      bool earlier = false;
+      for (int i = threadIdx.x; i < B; i += kStepThreads) {
+        const bool same = slots[i] == slot;
+        earlier |= same && i < b;
+        later |= same && i > b;
+      }
+      const int found = (__any(earlier) ? 1 : 0) | (__any(later) ? 2 : 0);
+      __syncthreads();  // the last row's words have been read
+      if ((threadIdx.x & 63) == 0) named[threadIdx.x >> 6] = found;
+      __syncthreads();
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < kStepThreads / 64; ++w) all |= named[w];
+      if (all & 1) continue;
+      later = all & 2;
     }
-    float* at = states + static_cast<int64_t>(slot) * channels + c;
-    float now = *at;
-    for (int i = b; i < B; ++i) {
-      if (i > b && (!slots || slots[i] != slot)) continue;
-      float a, w;
-      gate_of<FORM>(Elem<T>::load(row_of<T>(gate, i, h), j), a, w);
-      now = fmaf(a, now, w * Elem<T>::load(row_of<T>(x, i, h), j));
-      Elem<T>::store(row_of<T>(out, i, h), j, now);
+    for (int i = b;;) {
+      float g[V], v[V];
+      P::unpack(gw, g);
+      P::unpack(xw, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float a, keep;
+        gate_of<FORM>(g[j], a, keep);
+        now[j] = fmaf(a, now[j], keep * v[j]);
+      }
+      if (in) {
+        T* o = row_of<T>(out, i, h) + start;
+        if (shift == 0) {
+          P::keep(o, now);
+        } else {
+#pragma unroll
+          for (int j = 1; j < V; ++j)
+            if (j >= shift) Elem<T>::store(o, j, now[j]);
+        }
+      }
+      if (!later) break;
+      do ++i;
+      while (i < B && slots[i] != slot);
+      if (i >= B) break;
+      gw = P::load(row_of<T>(gate, i, h) + start);
+      xw = P::load(row_of<T>(x, i, h) + start);
     }
-    *at = now;
+    if (in) {
+      if (shift == 0) {
+        Pack<float, V>::keep(state, now);
+      } else {
+#pragma unroll
+        for (int j = 1; j < V; ++j)
+          if (j >= shift) state[j] = now[j];
+      }
+    }
   }
 }
 
 }  // namespace
-
-#define RET_BY_FORM_AND_TYPE(kernel, ...)                                              \
-  do {                                                                                 \
-    if (dtype == 0) {                                                                  \
-      if (form == 0) kernel<float, 0><<<grid, kThreads, 0, stream>>>(__VA_ARGS__);     \
-      else kernel<float, 1><<<grid, kThreads, 0, stream>>>(__VA_ARGS__);               \
-    } else {                                                                           \
-      if (form == 0) kernel<uint16_t, 0><<<grid, kThreads, 0, stream>>>(__VA_ARGS__);  \
-      else kernel<uint16_t, 1><<<grid, kThreads, 0, stream>>>(__VA_ARGS__);            \
-    }                                                                                  \
-  } while (0)
 
 namespace {
 
@@ -677,8 +722,30 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
 hipError_t launch_gated_recurrence_step(int form, int dtype, const View& x, const View& gate, const View& h, int B,
                                         int H, int d, float* states, int nstates, const int* slots,
                                         hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((H * d + kThreads - 1) / kThreads), B < 65535 ? B : 65535);
-  RET_BY_FORM_AND_TYPE(step_kernel, x, gate, h, B, H, d, states, nstates, slots);
+  // Heads that lie one behind the other are one long head.
+  if (x.sh == (H > 1 ? d : 0) && gate.sh == x.sh && h.sh == x.sh) {
+    d *= H;
+    H = 1;
+  }
+  const int vec = d < (dtype == 0 ? 4 : 8) ? 1 : dtype == 0 ? 4 : 8;
+  const int64_t pieces = static_cast<int64_t>((d + vec - 1) / vec) * H;
+  const dim3 grid(static_cast<unsigned>((pieces + kStepThreads - 1) / kStepThreads), B < 65535 ? B : 65535);
+#define RET_STEP(T, FORM, V) \
+  step_kernel<T, FORM, V><<<grid, kStepThreads, 0, stream>>>(x, gate, h, B, H, d, states, nstates, slots)
+#define RET_STEP_VEC(T, FORM, V)              \
+  do {                                        \
+    if (vec == V) RET_STEP(T, FORM, V);       \
+    else RET_STEP(T, FORM, 1);                \
+  } while (0)
+  if (dtype == 0) {
+    if (form == 0) RET_STEP_VEC(float, 0, 4);
+    else RET_STEP_VEC(float, 1, 4);
+  } else {
+    if (form == 0) RET_STEP_VEC(uint16_t, 0, 8);
+    else RET_STEP_VEC(uint16_t, 1, 8);
+  }
+#undef RET_STEP_VEC
+#undef RET_STEP
   return hipGetLastError();
 }
 

@@ -144,80 +144,82 @@ struct Part {
   }
 };
 
-// What the waves of a row exchange: [0] its moments (two sets, used in turn),
-// [1] the backward's two sums.
+// What the waves of a row exchange, in two sets used in turn: a fast wave
+// writes a row's set while a slow one may still read the last row's.
 template <int L>
 struct RowShared {
-  float2 moment[2][L / 64 > 0 ? L / 64 : 1];
-  float2 sums[L / 64 > 0 ? L / 64 : 1];
+  float4 part[2][L / 64 > 0 ? L / 64 : 1];
 };
 
-// Mean and 1 / deviation of a row. Across waves each wave's sum and squared
-// deviations from its own mean are joined: M2 = sum M2_w + n_w (mean_w - mean)^2.
-template <int L, int V, int K, bool MASK>
-__device__ __forceinline__ void row_moments(const float (&x)[V * K], const Part<L, V, K, MASK>& part, int d,
-                                            const NormArgs& n, RowShared<L>& shared, int turn, float& mean,
-                                            float& rstd) {
-  constexpr int E = V * K, W = L / 64;
+// Mean and 1 / deviation of the row v; with BACK also s1 = the mean of q and
+// s2 = the mean of q xhat. Each wave takes its sums about its own mean:
+//   M2 = sum M2_w + n_w (mean_w - mean)^2
+//   sum q (v - mean) = sum over waves of C_w + Q_w (mean_w - mean)
+// with Q_w the wave's sum of q and C_w that of q (v - mean_w), so that one
+// exchange joins them, with nothing lost to a mean far from 0. q is 0 for
+// channels that are not the thread's own.
+template <bool BACK, int L, int V, int K, bool MASK>
+__device__ __forceinline__ void row_stats(const float (&v)[V * K], const float (&q)[V * K],
+                                          const Part<L, V, K, MASK>& part, int d, const NormArgs& n,
+                                          RowShared<L>& shared, int turn, float& mean, float& rstd, float& s1,
+                                          float& s2) {
+  constexpr int E = V * K, W = L / 64, LW = L < 64 ? L : 64;
   const float inv = 1.0f / d;
-  float own_mean = 0.0f, sum = 0.0f, m2 = 0.0f;
-  const int wave = L > 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const int lane = threadIdx.x & 63, wave = L > 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  float sum = 0.0f, m2 = 0.0f, Q = 0.0f, C = 0.0f;
+  mean = 0.0f;
   if (!n.rms) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum += x[e];
-    sum = lanes_sum<(L < 64 ? L : 64)>(sum);
+    for (int e = 0; e < E; ++e) sum += v[e];
+    sum = lanes_sum<LW>(sum);
     if constexpr (L > 64) {
       const int own = Part<L, V, K, MASK>::count(wave, d);
-      own_mean = own > 0 ? sum / own : 0.0f;
+      mean = own > 0 ? sum / own : 0.0f;
     } else {
-      own_mean = sum * inv;
+      mean = sum * inv;
     }
   }
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float e = part.own(k, j) ? x[k * V + j] - own_mean : 0.0f;
+      const float e = part.own(k, j) ? v[k * V + j] - mean : 0.0f;
       m2 = fmaf(e, e, m2);
-    }
-  m2 = lanes_sum<(L < 64 ? L : 64)>(m2);
-  mean = own_mean;
-  if constexpr (L > 64) {
-    if ((threadIdx.x & 63) == 0) shared.moment[turn][wave] = make_float2(sum, m2);
-    lds_only_barrier();
-    sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) sum += shared.moment[turn][w].x;
-    mean = n.rms ? 0.0f : sum * inv;
-    m2 = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float2 m = shared.moment[turn][w];
-      m2 += m.y;
-      const int own = Part<L, V, K, MASK>::count(w, d);
-      if (!n.rms && own > 0) {
-        const float e = m.x / own - mean;
-        m2 = fmaf(own * e, e, m2);
+      if (BACK) {
+        Q += q[k * V + j];
+        C = fmaf(q[k * V + j], e, C);
       }
+    }
+  m2 = lanes_sum<LW>(m2);
+  if (BACK) {
+    Q = lanes_sum<LW>(Q);
+    C = lanes_sum<LW>(C);
+  }
+  if constexpr (L > 64) {
+    if (lane == 0) shared.part[turn][wave] = make_float4(sum, m2, Q, C);
+    lds_only_barrier();
+    const int w = lane % W;
+    const float4 p = shared.part[turn][w];
+    m2 = p.y;
+    Q = p.z;
+    C = p.w;
+    if (!n.rms) {
+      const int own = Part<L, V, K, MASK>::count(w, d);
+      mean = lanes_sum<W>(p.x) * inv;
+      const float off = own > 0 ? p.x / own - mean : 0.0f;
+      m2 = fmaf(own * off, off, m2);
+      C = fmaf(Q, off, C);
+    }
+    m2 = lanes_sum<W>(m2);
+    if (BACK) {
+      Q = lanes_sum<W>(Q);
+      C = lanes_sum<W>(C);
     }
   }
   rstd = 1.0f / sqrtf(fmaf(m2, inv, n.eps));
-}
-
-// Sums of a and b over the row.
-template <int L>
-__device__ __forceinline__ void row_sums(float& a, float& b, RowShared<L>& shared) {
-  a = lanes_sum<(L < 64 ? L : 64)>(a);
-  b = lanes_sum<(L < 64 ? L : 64)>(b);
-  if constexpr (L > 64) {
-    if ((threadIdx.x & 63) == 0) shared.sums[threadIdx.x >> 6] = make_float2(a, b);
-    lds_only_barrier();
-    a = b = 0.0f;
-#pragma unroll
-    for (int w = 0; w < L / 64; ++w) {
-      a += shared.sums[w].x;
-      b += shared.sums[w].y;
-    }
+  if (BACK) {
+    s1 = n.rms ? 0.0f : Q * inv;
+    s2 = C * rstd * inv;
   }
 }
 
@@ -267,9 +269,9 @@ gated_norm_kernel(View o, View gate, View y, int rows, int N, int d, NormArgs n)
     const auto ow = part.load(at<const T>(o, rb, h, rn));
     auto gw = ow;
     if (gate.data) gw = part.load(at<const T>(gate, rb, h, rn));
-    float x[E], gv[E], mean, rstd;
+    float x[E], gv[E], mean, rstd, s1, s2;
     part.values(ow, x);
-    row_moments(x, part, d, n, shared, 0, mean, rstd);
+    row_stats<false>(x, x, part, d, n, shared, 0, mean, rstd, s1, s2);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = fmaf((x[e] - mean) * rstd, w[e], b[e]);
     if (gate.data) {
@@ -282,18 +284,21 @@ gated_norm_kernel(View o, View gate, View y, int rows, int N, int d, NormArgs n)
 }
 
 // The workgroup's sums of SUMS parameters, from its G groups' registers, to
-// its row of the partial sums.
+// its row of the partial sums; those whose bit is set in `wanted`.
 template <int SUMS, int G, typename P>
-__device__ __forceinline__ void leave_sums(const P& part, const float (&sums)[SUMS][P::E], float* to, int d) {
+__device__ __forceinline__ void leave_sums(const P& part, const float (&sums)[SUMS][P::E], float* to, int d,
+                                           uint32_t wanted) {
   if constexpr (G == 1) {
 #pragma unroll
-    for (int s = 0; s < SUMS; ++s) part.put(to + static_cast<int64_t>(s) * d, sums[s]);
+    for (int s = 0; s < SUMS; ++s)
+      if (wanted >> s & 1) part.put(to + static_cast<int64_t>(s) * d, sums[s]);
   } else {
     // One parameter at a time, to keep the LDS at 16 KiB.
     constexpr int width = kThreads * P::E / G;
     __shared__ float all[G][width];
 #pragma unroll
     for (int s = 0; s < SUMS; ++s) {
+      if (!(wanted >> s & 1)) continue;
       __syncthreads();
       part.put(all[threadIdx.x / (kThreads / G)], sums[s]);
       __syncthreads();
@@ -310,7 +315,7 @@ __device__ __forceinline__ void leave_sums(const P& part, const float (&sums)[SU
 template <typename T, int L, int V, int K, bool MASK>
 __global__ void __launch_bounds__(kThreads)
 gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, int rows, int N, int d, NormArgs n,
-                           float* partial) {
+                           float* partial, uint32_t wanted) {
   constexpr int E = V * K, G = kThreads / L;
   typedef Part<L, V, K, MASK> P;
   __shared__ RowShared<L> shared;
@@ -321,59 +326,58 @@ gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, in
   part.params(n.bias ? n.bias + static_cast<int64_t>(h) * d : nullptr, 0.0f, b);
 #pragma unroll
   for (int e = 0; e < E; ++e) sums[0][e] = sums[1][e] = 0.0f;
-  const float inv = 1.0f / d;
   const int step = gridDim.x * G;
   RowWalk row(blockIdx.x * G + g, step, N);
-  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next()) {
+  typename P::template Raw<T> ow, dw, gw;
+  auto load = [&](bool live) {
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    ow = part.load(at<const T>(o, rb, h, rn));
+    dw = part.load(at<const T>(dy, rb, h, rn));
+    if (gate.data) gw = part.load(at<const T>(gate, rb, h, rn));
+  };
+  load(blockIdx.x * G + g < rows);
+  for (int64_t base = blockIdx.x * G; base < rows; base += step) {
     const bool live = base + g < rows;
     const int rb = live ? row.b : 0, rn = live ? row.n : 0;
-    const auto ow = part.load(at<const T>(o, rb, h, rn));
-    const auto dw = part.load(at<const T>(dy, rb, h, rn));
-    auto gw = ow;
-    if (gate.data) gw = part.load(at<const T>(gate, rb, h, rn));
-    float x[E], q[E], mean, rstd;
+    float x[E], dyv[E], q[E], gv[E], mean, rstd, s1, s2;
     part.values(ow, x);
-    row_moments(x, part, d, n, shared, 0, mean, rstd);
-    part.values(dw, q);
+    part.values(dw, dyv);
+    if (gate.data) part.values(gw, gv);
+    row.next();
+    if (base + step < rows) load(base + step + g < rows);  // the next row comes while this one is worked on
     if (!live) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) q[e] = 0.0f;
+      for (int e = 0; e < E; ++e) dyv[e] = 0.0f;
     }
+    float slope[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = (x[e] - mean) * rstd;
-    if (gate.data) {
-      float gv[E];
-      part.values(gw, gv);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
+    for (int e = 0; e < E; ++e) {  // dyv is 0 for channels that are not the thread's own
+      q[e] = dyv[e];
+      if (gate.data) {
         float s, less;
         sigmoid_pair(gv[e], s, less);
-        const float slope = s * fmaf(gv[e], less, 1.0f), z = fmaf(x[e], w[e], b[e]);
-        const float dyv = q[e];
-        q[e] = dyv * (gv[e] * s);
-        gv[e] = dyv * z * slope;
+        slope[e] = s * fmaf(gv[e], less, 1.0f);
+        q[e] *= gv[e] * s;
       }
-      if (live) part.store(at<T>(d_gate, rb, h, rn), gv);
-    }
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {  // q is 0 for channels that are not the thread's own
-      sums[0][e] = fmaf(q[e], x[e], sums[0][e]);
       sums[1][e] += q[e];
-      q[e] *= w[e];
-      s1 += q[e];
-      s2 = fmaf(q[e], x[e], s2);
     }
-    row_sums<L>(s1, s2, shared);
-    s1 = n.rms ? 0.0f : s1 * inv;
-    s2 *= inv;
+    float qw[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = rstd * (q[e] - s1 - x[e] * s2);
+    for (int e = 0; e < E; ++e) qw[e] = q[e] * w[e];
+    row_stats<true>(x, qw, part, d, n, shared, 0, mean, rstd, s1, s2);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] = (x[e] - mean) * rstd;
+      sums[0][e] = fmaf(q[e], x[e], sums[0][e]);
+      if (gate.data) gv[e] = dyv[e] * fmaf(x[e], w[e], b[e]) * slope[e];
+      q[e] = rstd * (qw[e] - s1 - x[e] * s2);
+    }
+    if (gate.data && live) part.store(at<T>(d_gate, rb, h, rn), gv);
     if (live) part.store(at<T>(d_o, rb, h, rn), q);
   }
   if (partial)
     leave_sums<kGatedNormSums, G, P>(
-        part, sums, partial + (static_cast<int64_t>(h) * gridDim.x + blockIdx.x) * kGatedNormSums * d, d);
+        part, sums, partial + (static_cast<int64_t>(h) * gridDim.x + blockIdx.x) * kGatedNormSums * d, d, wanted);
 }
 
 // out[k][head * d + c] = sum over parts of partial[head][part][k][c]: 16
@@ -419,6 +423,27 @@ hipError_t sum_params(const float* partial, int heads, int parts, int sums, int 
 
 constexpr int threads_of(int L) { return L > kThreads ? L : kThreads; }
 
+// A thread's parameters at p (null: never asked for): in registers while its
+// values are few, else read again for each row (from the caches).
+template <typename P>
+struct Held {
+  static constexpr bool kHold = P::E <= 8;
+  const P& part;
+  const float* p;
+  float v[kHold ? P::E : 1];
+  __device__ __forceinline__ Held(const P& part, const float* p) : part(part), p(p) {
+    if constexpr (kHold) part.params(p, 0.0f, v);
+  }
+  __device__ __forceinline__ void get(float (&x)[P::E]) const {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int e = 0; e < P::E; ++e) x[e] = v[e];
+    } else {
+      part.params(p, 0.0f, x);
+    }
+  }
+};
+
 template <typename T, typename TR, int L, int V, int K, bool MASK>
 __global__ void __launch_bounds__(threads_of(L))
 residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int D, NormArgs n, const float* scale,
@@ -426,7 +451,9 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
   constexpr int E = V * K, G = threads_of(L) / L;
   __shared__ RowShared<L> shared;
   const int g = threadIdx.x / L;
-  const Part<L, V, K, MASK> part(threadIdx.x % L, D);
+  typedef Part<L, V, K, MASK> P;
+  const P part(threadIdx.x % L, D);
+  const Held<P> scales(part, scale), weights(part, n.weight), biases(part, n.bias);
   const int step = gridDim.x * G;
   RowWalk row(blockIdx.x * G + g, step, N);
   int turn = 0;
@@ -435,10 +462,10 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
     const int rb = live ? row.b : 0, rn = live ? row.n : 0;
     const auto rw = part.load(at<const TR>(residual, rb, 0, rn));
     const auto xw = part.load(at<const T>(x, rb, 0, rn));
-    float v[E], p[E], mean, rstd;
+    float v[E], p[E], mean, rstd, s1, s2;
     part.values(xw, v);
     if (scale) {
-      part.params(scale, 1.0f, p);
+      scales.get(p);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] *= p[e];
     }
@@ -446,16 +473,16 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = fmaf(alpha, p[e], v[e]);
     if (live) part.store(at<TR>(r, rb, 0, rn), v);
-    row_moments(v, part, D, n, shared, turn, mean, rstd);
+    row_stats<false>(v, v, part, D, n, shared, turn, mean, rstd, s1, s2);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = (v[e] - mean) * rstd;
     if (n.weight) {
-      part.params(n.weight, 1.0f, p);
+      weights.get(p);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] *= p[e];
     }
     if (n.bias) {
-      part.params(n.bias, 0.0f, p);
+      biases.get(p);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += p[e];
     }
@@ -463,16 +490,18 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
   }
 }
 
+// The row is r or, with `residual`, formed again from it and x.
 template <typename T, typename TR, int L, int V, int K, bool MASK>
-__global__ void __launch_bounds__(threads_of(L))
-residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dres, int rows, int N, int D, NormArgs n,
-                              const float* scale, float alpha, float* partial) {
+__global__ void __launch_bounds__(threads_of(L), V* K <= 8 || L == 1024 ? 4 : 2)
+residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, View dx, View dres, int rows, int N,
+                              int D, NormArgs n, const float* scale, float alpha, float* partial, uint32_t wanted) {
   constexpr int E = V * K, G = threads_of(L) / L;
+  constexpr bool kEarly = L <= 512;
   typedef Part<L, V, K, MASK> P;
   __shared__ RowShared<L> shared;
   const int g = threadIdx.x / L;
   const P part(threadIdx.x % L, D);
-  const float inv = 1.0f / D;
+  const Held<P> scales(part, scale), weights(part, n.weight);
   float sums[kResidualNormSums][E];
 #pragma unroll
   for (int s = 0; s < kResidualNormSums; ++s)
@@ -480,53 +509,67 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dr
     for (int e = 0; e < E; ++e) sums[s][e] = 0.0f;
   const int step = gridDim.x * G;
   RowWalk row(blockIdx.x * G + g, step, N);
-  for (int64_t base = blockIdx.x * G; base < rows; base += step, row.next()) {
+  const View& from = residual.data ? residual : r;
+  typename P::template Raw<TR> vw, sw;
+  typename P::template Raw<T> gw, xw;
+  auto load = [&](bool live) {
+    const int rb = live ? row.b : 0, rn = live ? row.n : 0;
+    vw = part.load(at<const TR>(from, rb, 0, rn));
+    if (x.data) xw = part.load(at<const T>(x, rb, 0, rn));
+    gw = part.load(at<const T>(dy, rb, 0, rn));
+    if (dr.data) sw = part.load(at<const TR>(dr, rb, 0, rn));
+  };
+  load(blockIdx.x * G + g < rows);
+  int turn = 0;
+  for (int64_t base = blockIdx.x * G; base < rows; base += step, turn ^= 1) {
     const bool live = base + g < rows;
     const int rb = live ? row.b : 0, rn = live ? row.n : 0;
-    const auto vw = part.load(at<const TR>(r, rb, 0, rn));
-    const auto gw = part.load(at<const T>(dy, rb, 0, rn));
-    auto sw = vw;
-    if (dr.data) sw = part.load(at<const TR>(dr, rb, 0, rn));
-    auto xw = gw;
-    if (x.data) xw = part.load(at<const T>(x, rb, 0, rn));
-    float v[E], q[E], p[E], mean, rstd;
+    float v[E], q[E], p[E], mean, rstd, s1, s2;
     part.values(vw, v);
-    row_moments(v, part, D, n, shared, 0, mean, rstd);
     part.values(gw, q);
+    const auto sw_now = sw;
+    const auto xw_now = xw;
+    row.next();
+    // The next row comes while this one is worked on, where registers allow.
+    if (kEarly && base + step < rows) load(base + step + g < rows);
+    if (residual.data) {
+      float b[E];
+      part.values(xw_now, b);
+      if (scale) {
+        scales.get(p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) b[e] *= p[e];
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = fmaf(alpha, v[e], b[e]);
+    }
     if (!live) {
 #pragma unroll
       for (int e = 0; e < E; ++e) q[e] = 0.0f;
     }
+    float qw[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (v[e] - mean) * rstd;
+    for (int e = 0; e < E; ++e) qw[e] = q[e];
+    if (n.weight) {
+      weights.get(p);
+#pragma unroll
+      for (int e = 0; e < E; ++e) qw[e] *= p[e];
+    }
+    row_stats<true>(v, qw, part, D, n, shared, turn, mean, rstd, s1, s2);
 #pragma unroll
     for (int e = 0; e < E; ++e) {  // q is 0 for channels that are not the thread's own
+      v[e] = (v[e] - mean) * rstd;
       sums[1][e] = fmaf(q[e], v[e], sums[1][e]);
       sums[2][e] += q[e];
+      q[e] = rstd * (qw[e] - s1 - v[e] * s2);
     }
-    if (n.weight) {
-      part.params(n.weight, 1.0f, p);
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[e] *= p[e];
-    }
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      s1 += q[e];
-      s2 = fmaf(q[e], v[e], s2);
-    }
-    row_sums<L>(s1, s2, shared);
-    s1 = n.rms ? 0.0f : s1 * inv;
-    s2 *= inv;
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = rstd * (q[e] - s1 - v[e] * s2);
     if (dr.data) {
-      part.values(sw, p);
+      part.values(sw_now, p);
 #pragma unroll
       for (int e = 0; e < E; ++e) q[e] += p[e];
     }
     if (x.data) {
-      part.values(xw, p);  // 0 for channels that are not the thread's own
+      part.values(xw_now, p);  // 0 for channels that are not the thread's own
 #pragma unroll
       for (int e = 0; e < E; ++e) sums[0][e] = live ? fmaf(q[e], p[e], sums[0][e]) : sums[0][e];
     }
@@ -535,22 +578,27 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dr
     if (live) part.store(at<TR>(dres, rb, 0, rn), v);
     if (dx.data) {
       if (scale) {
-        part.params(scale, 1.0f, p);
+        scales.get(p);
 #pragma unroll
         for (int e = 0; e < E; ++e) q[e] *= p[e];
       }
       if (live) part.store(at<T>(dx, rb, 0, rn), q);
     }
+    if (!kEarly && base + step < rows) load(base + step + g < rows);
   }
   if (partial)
     leave_sums<kResidualNormSums, G, P>(part, sums,
-                                        partial + static_cast<int64_t>(blockIdx.x) * kResidualNormSums * D, D);
+                                        partial + static_cast<int64_t>(blockIdx.x) * kResidualNormSums * D, D,
+                                        wanted);
 }
 
 // ---------------------------------------------------------------------------
-// Which instance takes a width: the fewest lanes that hold it at 16 values
-// each (8 of bf16 or 4 of fp32 to an access), one value a lane for rows
-// shorter than an access.
+// Which instance takes a width: the fewest lanes that hold it at 8 values each
+// (one access of bf16, two of fp32; four for narrow fp32 heads, 16 where 8
+// would need more than a wave for a row up to 1024 or more than a workgroup),
+// one value a lane for rows shorter than an access. Rows of 4096 at 16 values in
+// 256 threads against 8 in 512, forward with an fp32 stream: 162 and 152 us at
+// 16384 rows.
 
 #define RET_ROW(kernel, L, V, K, ...)                                                \
   do {                                                                               \
@@ -576,8 +624,8 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View dx, View dr
     if (d <= 64 * V) RET_ROW(kernel, 64, V, 1, __VA_ARGS__);                         \
     if (d <= 1024) RET_ROW(kernel, 64, V, 16 / V, __VA_ARGS__);                      \
     if (d <= 2048) RET_ROW(kernel, 256, V, 8 / V, __VA_ARGS__);                      \
-    if (d <= 4096) RET_ROW(kernel, 256, V, 16 / V, __VA_ARGS__);                     \
-    if (d <= 8192) RET_ROW(kernel, 512, V, 16 / V, __VA_ARGS__);                     \
+    if (d <= 4096) RET_ROW(kernel, 512, V, 8 / V, __VA_ARGS__);                      \
+    if (d <= 8192) RET_ROW(kernel, 1024, V, 8 / V, __VA_ARGS__);                     \
     RET_ROW(kernel, 1024, V, 16 / V, __VA_ARGS__);                                   \
   } while (0)
 
@@ -610,23 +658,23 @@ namespace {
 
 hipError_t gated_norm_backward(int dtype, const View& dy, const View& o, const View& gate, const View& d_o,
                                const View& d_gate, int parts, int H, int rows, int N, int d, const NormArgs& norm,
-                               float* partial, hipStream_t stream) {
+                               float* partial, uint32_t wanted, hipStream_t stream) {
   const dim3 grid(parts, H);
 #define RET_LAUNCH(L, V, K, MASK, T)                                                                             \
   gated_norm_backward_kernel<T, L, V, K, MASK><<<grid, kThreads, 0, stream>>>(dy, o, gate, d_o, d_gate, rows, N, \
-                                                                              d, norm, partial)
+                                                                              d, norm, partial, wanted)
   if (dtype == 0) RET_HEAD_ROWS(RET_LAUNCH, 4, float);
   RET_HEAD_ROWS(RET_LAUNCH, 8, uint16_t);
 #undef RET_LAUNCH
 }
 
 hipError_t residual_norm_backward(int dtype, int stream_dtype, const View& dy, const View& dr, const View& r,
-                                  const View& x, const View& dx, const View& dres, int parts, int rows, int N, int d,
+                                  const View& x, const View& residual, const View& dx, const View& dres, int parts, int rows, int N, int d,
                                   const NormArgs& norm, const float* scale, float alpha, float* partial,
-                                  hipStream_t stream) {
+                                  uint32_t wanted, hipStream_t stream) {
 #define RET_LAUNCH(L, V, K, MASK, T, TR)                                                              \
   residual_norm_backward_kernel<T, TR, L, V, K, MASK><<<parts, threads_of(L), 0, stream>>>(           \
-      dy, dr, r, x, dx, dres, rows, N, d, norm, scale, alpha, partial)
+      dy, dr, r, x, residual, dx, dres, rows, N, d, norm, scale, alpha, partial, wanted)
   if (dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 4, float, float);
   if (stream_dtype == 0) RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, float);
   RET_MODEL_ROWS(RET_LAUNCH, 8, uint16_t, uint16_t);
@@ -639,10 +687,11 @@ hipError_t launch_gated_norm_backward(int dtype, const View& grad_y, const View&
                                       const View& grad_o, const View& grad_gate, int B, int H, int N, int d,
                                       const NormArgs& norm, float* grad_weight, float* grad_bias, void* workspace,
                                       hipStream_t stream) {
-  const int rows = B * N, parts = norm_parts(H, rows, rows_at_once(d, dtype, true), kBackwardGroups);
+  const int rows = B * N, parts = norm_parts(H, rows, rows_at_once(d, dtype, true), gated_back_groups(H, rows, rows_at_once(d, dtype, true)));
   float* partial = grad_weight || grad_bias ? static_cast<float*>(workspace) : nullptr;
   const hipError_t e =
-      gated_norm_backward(dtype, grad_y, o, gate, grad_o, grad_gate, parts, H, rows, N, d, norm, partial, stream);
+      gated_norm_backward(dtype, grad_y, o, gate, grad_o, grad_gate, parts, H, rows, N, d, norm, partial,
+                          (grad_weight ? 1u : 0u) | (grad_bias ? 2u : 0u), stream);
   if (e != hipSuccess || !partial) return e;
   return sum_params(partial, H, parts, kGatedNormSums, d, grad_weight, grad_bias, nullptr, stream);
 }
@@ -661,16 +710,18 @@ hipError_t launch_residual_norm(int dtype, int stream_dtype, const View& x, cons
 }
 
 hipError_t launch_residual_norm_backward(int dtype, int stream_dtype, const View& grad_y, const View& grad_r,
-                                         const View& r, const View& x, const View& grad_x, const View& grad_residual,
-                                         int B, int N, int d, const NormArgs& norm, const float* scale, float alpha,
+                                         const View& r, const View& x, const View& residual, const View& grad_x,
+                                         const View& grad_residual, int B, int N, int d, const NormArgs& norm, const float* scale, float alpha,
                                          float* grad_scale, float* grad_weight, float* grad_bias, void* workspace,
                                          hipStream_t stream) {
-  const int rows = B * N, parts = norm_parts(1, rows, rows_at_once(d, dtype, false), kBackwardGroups);
+  const int rows = B * N, parts = norm_parts(1, rows, rows_at_once(d, dtype, false), residual_back_groups(d));
   float* partial = grad_scale || grad_weight || grad_bias ? static_cast<float*>(workspace) : nullptr;
   View xs = x;
-  if (!grad_scale) xs.data = nullptr;
-  const hipError_t e = residual_norm_backward(dtype, stream_dtype, grad_y, grad_r, r, xs, grad_x, grad_residual, parts,
-                                              rows, N, d, norm, scale, alpha, partial, stream);
+  if (!grad_scale && !residual.data) xs.data = nullptr;
+  const hipError_t e = residual_norm_backward(dtype, stream_dtype, grad_y, grad_r, r, xs, residual, grad_x, grad_residual, parts,
+                                              rows, N, d, norm, scale, alpha, partial,
+                                              (grad_scale ? 1u : 0u) | (grad_weight ? 2u : 0u) | (grad_bias ? 4u : 0u),
+                                              stream);
   if (e != hipSuccess || !partial) return e;
   return sum_params(partial, 1, parts, kResidualNormSums, d, grad_scale, grad_weight, grad_bias, stream);
 }

@@ -43,8 +43,8 @@ hipError_t launch_residual_norm(int, int, const View&, const View&, const View&,
   return record();
 }
 hipError_t launch_residual_norm_backward(int, int, const View&, const View&, const View&, const View&, const View&,
-                                         const View&, int, int, int, const NormArgs&, const float*, float, float*,
-                                         float*, float*, void*, hipStream_t) {
+                                         const View&, const View&, int, int, int, const NormArgs&, const float*,
+                                         float, float*, float*, float*, void*, hipStream_t) {
   return record();
 }
 

@@ -87,11 +87,12 @@ def rnorm(lib, B=2, N=10, D=64, dtype=1, stream=1, x=A[0], res=A[1], y=A[2], r=A
                                        norm or _norm(), scale, alpha, None)
 
 
-def rnorm_back(lib, B=2, N=10, D=64, dr=A[1], x=A[3], dx=A[4], dres=A[5], dscale=A[6], dw=A[7], db=A[8], ws=WS,
+def rnorm_back(lib, B=2, N=10, D=64, dr=A[1], r=A[2], x=A[3], res=None, dx=A[4], dres=A[5], dscale=A[6], dw=A[7], db=A[8], ws=WS,
                ws_bytes=1 << 40, alpha=1.0):
     st = (N * D, 0, D)
-    return lib.retention_residual_norm_backward(_v(A[0], *st), _v(dr, *st) if dr else None, _v(A[2], *st),
-                                                _v(x, *st) if x else None, _v(dx, *st) if dx else None, _v(dres, *st), B, N, D,
+    return lib.retention_residual_norm_backward(_v(A[0], *st), _v(dr, *st) if dr else None,
+                                                _v(r, *st) if r else None, _v(x, *st) if x else None,
+                                                _v(res, *st) if res else None, _v(dx, *st) if dx else None, _v(dres, *st), B, N, D,
                                                 1, 1, _norm(), None, alpha, dscale, dw, db, ws, ws_bytes, None)
 
 
@@ -174,7 +175,7 @@ def test_residual_norm_refuses(lib, kw):
     assert rnorm(lib, **kw) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(x=None), dict(dres=A[4]), dict(dx=A[2]), dict(dscale=A[0]), dict(ws=None), dict(ws_bytes=8),
+@pytest.mark.parametrize("kw", [dict(x=None), dict(r=None), dict(res=A[9], r=None, x=None, dscale=None), dict(res=A[5]), dict(dres=A[4]), dict(dx=A[2]), dict(dscale=A[0]), dict(ws=None), dict(ws_bytes=8),
                                 dict(alpha=float("nan")), dict(db=A[7])])
 def test_residual_norm_backward_refuses(lib, kw):
     assert rnorm_back(lib, **kw) == INVALID
@@ -189,7 +190,7 @@ def test_valid_calls_reach_the_launchers(lib):
         (backward, {}), (backward, dict(form=1, x=None)), (backward, dict(ds=A[6], ds_in=A[6], s_in=A[7])),
         (step, {}), (step, dict(slots=A[5], n=2)), (gnorm, {}), (gnorm, dict(gate=None)), (gnorm_back, {}),
         (gnorm_back, dict(dw=None, db=None, ws=None)), (gnorm_back, dict(gate=None, dg=None)), (rnorm, {}),
-        (rnorm, dict(stream=0)), (rnorm_back, {}), (rnorm_back, dict(dr=None, x=None, dx=None, dscale=None)),
+        (rnorm, dict(stream=0)), (rnorm_back, {}), (rnorm_back, dict(dr=None, x=None, dx=None, dscale=None)), (rnorm_back, dict(r=None, res=A[9])),
         (rnorm_back, dict(dscale=None, dw=None, db=None, ws=None)),
     ]
     for fn, kw in calls:

@@ -454,6 +454,20 @@ def test_residual_norm_matches_the_oracle(shape, dtype, stream, rms, scaled, alp
             _check(t, ref, e, what)
     shared = not scaled and alpha == 1.0 and dtype == stream
     assert (got[0] is got[1]) == shared
+    # From x and the residual instead of r: the gradients at the row before its rounding. What forming it rounds (4 steps
+    # of its terms, e_r) changes the normed row like a change of the row itself: by at most three times that over the
+    # deviation, within ROW of the magnitudes already counted.
+    got = ret.residual_norm_backward(place(dy), None, norm, grad_r=place(dr) if with_dr else None, x=xd, scale=sd, alpha=alpha,
+                                     residual=place(res))
+    torch.cuda.synchronize()
+    bargs = (dy, dr if with_dr else None, r_ref, w, EPS, rms, x, scale, alpha)
+    terms = np.abs(alpha * orc.f64(res)) + np.abs(orc.f64(x) * (1.0 if scale is None else orc.f64(scale)))
+    grow = 1 + float((terms.max(-1) / np.abs(r_ref).max(-1)).max())
+    refs, errs = orc.residual_norm_backward(*bargs), orc.residual_norm_backward_error(*bargs)
+    for t, ref, e, what, wanted in zip(got, refs, errs, ("grad_x", "grad_residual", "grad_scale", "grad_weight", "grad_bias"),
+                                       (True, True, scaled, "w" in which, "b" in which)):
+        if wanted:
+            _check(t, ref, grow * e, what + " from the residual")
 
 
 def test_constant_rows_and_huge_values():
