@@ -63,15 +63,16 @@ enum retention_gate_form {
  * cu_seqlens[s + 1] of the one row; max_len bounds the length of a sequence.
  * A sequence may be empty (its state passes through). Tokens outside every
  * sequence, or beyond max_len of one, are neither read nor written. Offsets
- * outside [0, N] are clamped into it. d <= 2^20 and token strides (stride_n)
+ * outside [0, N] are clamped into it. At most 2^20 sequences, d <= 2^20 and token strides (stride_n)
  * below 2^24 elements, else RET_ERR_UNSUPPORTED. Without cu_seqlens (NULL) `sequences`
  * must be B and max_len N.
  *
- * workspace: retention_gated_recurrence_workspace_bytes(...) bytes, 8-byte
- * aligned, its contents on entry do not matter; two calls that may overlap in time
+ * workspace: retention_gated_recurrence_workspace_bytes(...) bytes (packed:
+ * whether there are cu_seqlens; the same for the backward), 8-byte aligned, its contents on entry do not matter; two calls that may overlap in time
  * need one each.
  */
-size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int max_len, int d, int dtype);
+size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int N, int max_len, int packed, int d,
+                                                  int dtype);
 
 int retention_gated_recurrence(const retention_view_t* x, const retention_view_t* gate, const retention_view_t* h,
                                int B, int H, int N, int d, int form, int dtype, const float* state_in,

@@ -137,7 +137,7 @@ def declare_block(lib):
     vp, i, f, size = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     view, norm = ctypes.POINTER(View), ctypes.POINTER(NormStruct)
     workspace = [vp, size, vp]  # workspace, its bytes, stream
-    lib.retention_gated_recurrence_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.retention_gated_recurrence_workspace_bytes.argtypes = [i] * 7
     lib.retention_gated_recurrence_workspace_bytes.restype = size
     lib.retention_gated_recurrence.argtypes = [view] * 3 + [i] * 6 + [vp, vp, vp, i, i] + workspace
     lib.retention_gated_recurrence.restype = i

@@ -160,10 +160,16 @@ def _state_to_fill(t, name, shape, device):
     return _require(t, name, shape, torch.float32, device)
 
 
-def gated_recurrence_workspace_bytes(sequences, H, max_len, d, dtype=torch.bfloat16) -> int:
-    """Workspace bytes of gated_recurrence and its backward, for ``sequences`` of at most ``max_len`` tokens."""
+def gated_recurrence_workspace_bytes(sequences, H, N, d, dtype=torch.bfloat16, max_len=None) -> int:
+    """Workspace bytes of gated_recurrence and its backward: for ``sequences`` rows of N tokens or, with ``max_len``,
+    as many packed sequences of at most that length in one row of N tokens."""
     code = _lib.RET_BF16 if dtype == torch.bfloat16 else _lib.RET_F32
-    return int(_lib.load().retention_gated_recurrence_workspace_bytes(sequences, H, max_len, d, code))
+    return _scan_bytes(sequences, (1, H, N, d), N if max_len is None else max_len, max_len is not None, code)
+
+
+def _scan_bytes(S, dims, max_len, packed, code):
+    return int(_lib.load().retention_gated_recurrence_workspace_bytes(S, dims[1], dims[2], max_len, packed, dims[3],
+                                                                      code))
 
 
 def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: Union[bool, torch.Tensor] = False,
@@ -191,7 +197,7 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     if state_in is not None:
         _require(state_in, "state_in", states, torch.float32, dev)
     state_out = _state_to_fill(state_out, "state_out", states, dev)
-    nbytes = int(_lib.load().retention_gated_recurrence_workspace_bytes(S, dims[1], max_len, dims[3], dt))
+    nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
     _call("retention_gated_recurrence", dev, _seq_view(x), _seq_view(gate), _seq_view(out), *dims, code, dt,
           _ptr(state_in), _ptr(state_out), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have, _stream(x))
@@ -231,7 +237,7 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
         if t is not None:
             _require(t, name, states, torch.float32, dev)
     grad_state_in = _state_to_fill(grad_state_in, "grad_state_in", states, dev)
-    nbytes = int(_lib.load().retention_gated_recurrence_workspace_bytes(S, dims[1], max_len, dims[3], dt))
+    nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
     _call("retention_gated_recurrence_backward", dev, _seq_view(grad_h), _seq_view(x), _seq_view(gate), _seq_view(h),
           _seq_view(grads[0]), _seq_view(grads[1]), *dims, code, dt, _ptr(state_in), _ptr(grad_state_out),

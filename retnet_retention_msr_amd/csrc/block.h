@@ -37,10 +37,14 @@ constexpr int kScanSigmoidBackRows = 16;  // of a wave of the sigmoid form's bac
 constexpr int kScanNarrowRows = 8;    // of a wave with one channel a lane
 struct ScanPlan {
   int vec, waves, wave_rows, rows;
-  int64_t units, tiles;
-  int64_t blocks;  // workgroups of the launch
-  size_t bytes;    // workspace
+  int64_t units, tiles;  // tiles of the longest sequence
+  int64_t slots;         // tiles of a slab over all sequences: the workspace's places
+  int64_t blocks;        // workgroups of the launch
+  size_t bytes;          // workspace
 };
+// The tiles of S packed sequences in N tokens have the slots floor(first token
+// / rows) + s + tile: no two share one, and there are at most N / rows + S,
+// however long the longest may be.
 // Workgroups of four waves where there are many units, of eight where there
 // are few. With many, most of the tiles in flight belong to different units
 // and wait for none of the others, and the smaller workgroups keep loads and
@@ -53,7 +57,7 @@ struct ScanPlan {
 // The sigmoid form's backward reads four tensors; waves of 16 tokens let it
 // hold them in 128 registers, four waves to a SIMD: 605 us against 705 with 32
 // at 8 x 8192 x 4096.
-inline ScanPlan plan_scan(int S, int H, int max_len, int d, int dtype, bool backward, int form) {
+inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, int dtype, bool backward, int form) {
   ScanPlan p{};
   p.vec = dtype == 0 ? 4 : 8;
   if (d < p.vec) p.vec = 1;
@@ -65,10 +69,12 @@ inline ScanPlan plan_scan(int S, int H, int max_len, int d, int dtype, bool back
   p.waves = static_cast<int>(waves < most ? waves : most);
   p.rows = p.waves * p.wave_rows;
   p.tiles = (static_cast<int64_t>(max_len) + p.rows - 1) / p.rows;
-  p.blocks = p.units > (int64_t{1} << 40) ? p.units : p.units * p.tiles;
+  const int64_t columns = p.units / S;
+  p.slots = packed && p.tiles > 1 ? N / p.rows + S : p.tiles * S;
+  p.blocks = p.units > (int64_t{1} << 40) ? p.units : columns * p.slots;
   if (p.tiles > 1)
     p.bytes = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
-              static_cast<size_t>(p.blocks) * kScanChannels * (sizeof(uint64_t) + sizeof(uint32_t));
+              static_cast<size_t>(columns) * p.slots * kScanChannels * (sizeof(uint64_t) + sizeof(uint32_t));
   return p;
 }
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,

@@ -17,6 +17,7 @@ constexpr int64_t kMaxSpan = int64_t{1} << 46;  // elements a view may span
 constexpr int kMaxChannels = 1 << 20;           // d of the recurrence
 constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // elements; offsets within a wave's tokens are 32-bit
 constexpr int64_t kMaxBlocks = int64_t{1} << 30;
+constexpr int kMaxSequences = 1 << 20;
 
 int status_of(hipError_t e) { return e == hipSuccess ? RET_OK : RET_ERR_HIP; }
 bool valid_dtype(int dtype) { return dtype == RET_F32 || dtype == RET_BF16; }
@@ -136,10 +137,10 @@ int check_float_array(const float* p, int64_t n, Range* r) {
 
 // The largest of what the recurrence and its backward need in either form: one
 // workspace serves them all. 0 blocks where a launch would be out of range.
-ret::ScanPlan plan_any(int sequences, int H, int max_len, int d, int dtype) {
+ret::ScanPlan plan_any(int sequences, int H, int N, int max_len, bool packed, int d, int dtype) {
   ret::ScanPlan most{};
   for (int i = 0; i < 4; ++i) {
-    const ret::ScanPlan p = ret::plan_scan(sequences, H, max_len, d, dtype, i & 1, i >> 1);
+    const ret::ScanPlan p = ret::plan_scan(sequences, H, N, max_len, packed, d, dtype, i & 1, i >> 1);
     if (p.blocks > kMaxBlocks) return ret::ScanPlan{};
     most.blocks = most.blocks > p.blocks ? most.blocks : p.blocks;
     most.bytes = most.bytes > p.bytes ? most.bytes : p.bytes;
@@ -156,9 +157,9 @@ int check_sequences(int B, int H, int N, int d, int form, int dtype, const int* 
   if (sequences <= 0 || max_len <= 0) return RET_ERR_INVALID_ARG;
   if (cu ? B != 1 : (sequences != B || max_len != N)) return RET_ERR_INVALID_ARG;
   if (misaligned(cu, 4)) return RET_ERR_INVALID_ARG;
-  if (d > kMaxChannels) return RET_ERR_UNSUPPORTED;
+  if (d > kMaxChannels || (cu && sequences > kMaxSequences)) return RET_ERR_UNSUPPORTED;
   if (max_len > N) max_len = N;
-  const ret::ScanPlan plan = plan_any(sequences, H, max_len, d, dtype);
+  const ret::ScanPlan plan = plan_any(sequences, H, N, max_len, cu != nullptr, d, dtype);
   if (plan.blocks <= 0) return RET_ERR_UNSUPPORTED;
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || misaligned(workspace, 8)))
     return RET_ERR_INVALID_ARG;
@@ -185,9 +186,12 @@ int check_states(const float* from, const float* to, int64_t n, Ranges* ranges) 
 
 extern "C" {
 
-size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int max_len, int d, int dtype) {
-  if (sequences <= 0 || H <= 0 || max_len <= 0 || d <= 0 || d > kMaxChannels || !valid_dtype(dtype)) return 0;
-  const ret::ScanPlan plan = plan_any(sequences, H, max_len, d, dtype);
+size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int N, int max_len, int packed, int d,
+                                                  int dtype) {
+  if (sequences <= 0 || max_len <= 0 || d > kMaxChannels || (packed && sequences > kMaxSequences)) return 0;
+  if (!packed && max_len != N) return 0;
+  if (check_dims(packed ? 1 : sequences, H, N, d, dtype) != RET_OK) return 0;
+  const ret::ScanPlan plan = plan_any(sequences, H, N, max_len < N ? max_len : N, packed != 0, d, dtype);
   return plan.blocks > 0 ? plan.bytes : 0;
 }
 

@@ -126,9 +126,13 @@ def test_recurrence_limits(lib):
 
 def test_recurrence_workspace(lib):
     f = lib.retention_gated_recurrence_workspace_bytes
-    for bad in ((0, 1, 1, 1, 1), (1, 0, 1, 1, 1), (1, 1, 0, 1, 1), (1, 1, 1, 0, 1), (1, 1, 1, 1, 2)):
+    for bad in ((0, 1, 9, 9, 0, 1, 1), (1, 0, 9, 9, 0, 1, 1), (1, 1, 0, 0, 0, 1, 1), (1, 1, 9, 9, 0, 0, 1), (1, 1, 9, 9, 0, 1, 2),
+                (1, 1, 9, 8, 0, 1, 1), (1, 1, 9, 0, 1, 1, 1)):
         assert f(*bad) == 0
-    need = f(1, 3, 60000, 64, 1)
+    need = f(1, 3, 60000, 60000, 0, 64, 1)
+    assert need > 0 == f(1, 3, 32, 32, 0, 64, 1)
+    # A packed row's need goes with its tokens and the number of its sequences, not with their product.
+    assert f(64, 3, 60000, 60000, 1, 64, 1) < 2 * need
     if need:
         assert recurrence(lib, B=1, N=60000, ws=None) == INVALID
         assert recurrence(lib, B=1, N=60000, ws_bytes=need - 1) == INVALID

@@ -183,6 +183,44 @@ def test_packed_sequences(dtype, form, d, heads):
         assert bool((t.cpu()[..., left, :] == mark).all())
 
 
+@pytest.mark.parametrize("S, longest", [(70, 900), (300, 300), (4200, 9)])
+def test_many_packed_sequences(S, longest):
+    """More sequences than a wave has lanes (and than its square), a few longer than a tile: the result is that of the
+    rows padded to one length."""
+    _announce(f"{S} packed sequences")
+    d, rng = 24, np.random.default_rng(S)
+    lens = rng.integers(0, 6, S)
+    lens[rng.integers(0, S, 5)] = longest
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T, most = int(cu[-1]), int(lens.max())
+    x, g, dh = _randn((1, T, d), 1), _gate((1, T, d), 2, F32, "log"), _randn((1, T, d), 3)
+    s0, ds = _randn((S, d), 4).to(DEV), _randn((S, d), 5).to(DEV)
+    pad = np.full((S, most), T)
+    for i in range(S):
+        pad[i, :lens[i]] = np.arange(cu[i], cu[i + 1])
+    at = torch.from_numpy(pad)
+    rows = [torch.cat((t[0], torch.zeros(1, d)))[at].to(DEV) for t in (x, g, dh)]  # padding: a = 1, x = 0 keep the state
+    h_pad, s_pad = ret.gated_recurrence(rows[0], rows[1], "log", state_in=s0, state_out=True)
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    dev = [t.to(DEV) for t in (x, g, dh)]
+    h, s1 = ret.gated_recurrence(dev[0], dev[1], "log", state_in=s0, state_out=True, cu_seqlens=cud)
+    dx, dg, ds0 = ret.gated_recurrence_backward(dev[2], dev[0], dev[1], h, "log", state_in=s0, grad_state_out=ds,
+                                                grad_state_in=True, cu_seqlens=cud, max_len=most)
+    back = ret.gated_recurrence_backward(rows[2], rows[0], rows[1], h_pad, "log", state_in=s0, grad_state_out=ds, grad_state_in=True)
+    torch.cuda.synchronize()
+    live = at < T
+    # Both are the same recurrences in another tiling: twice the bound of one.
+    e, e_end = orc.recurrence_error(rows[0].cpu(), rows[1].cpu(), "log", s0.cpu())
+    _check(h[0], orc.f64(h_pad)[live.numpy()], 2 * e[live.numpy()], "h")
+    _check(s1, orc.f64(s_pad), 2 * e_end, "state")
+    errs = orc.recurrence_backward_error(rows[2].cpu(), rows[0].cpu(), rows[1].cpu(), h_pad.cpu(), "log", s0.cpu(), ds.cpu())
+    # grad_gate also takes the h of its own call, which differs by up to 2 e.
+    dh_err = 2 * np.concatenate((np.zeros((S, 1, d)), e[:, :-1]), 1) * np.abs(orc.f64(back[0])) * orc.decay(rows[1].cpu(), "log")[0]
+    _check(dx[0], orc.f64(back[0])[live.numpy()], 2 * errs[0][live.numpy()], "grad_x")
+    _check(dg[0], orc.f64(back[1])[live.numpy()], (2 * errs[1] + dh_err)[live.numpy()], "grad_gate")
+    _check(ds0, orc.f64(back[2]), 2 * errs[2], "grad_state_in")
+
+
 def test_offsets_out_of_range_are_clamped():
     _announce("offsets out of range")
     T, d = 40, 16
