@@ -359,8 +359,10 @@ def _run_own(s):
     y, r = ret.residual_norm(s["x"], s["res"], norm, scale=s["scale"], alpha=c["alpha"])
     if op == "rnorm":
         return y, r
+    # A bf16 r carries its rounding into the parameters' fp32 gradients; x and the residual give them exactly.
+    residual = s["res"] if s["res"].dtype != torch.float32 else None
     return (y, r, *ret.residual_norm_backward(s["dy"], r, norm, grad_r=s["dr"], x=s["x"], scale=s["scale"],
-                                              alpha=c["alpha"]))
+                                              alpha=c["alpha"], residual=residual))
 
 
 def run(state):
