@@ -72,12 +72,16 @@ def _last_contiguous(t, name):
 def _same(t, name, like, dtype=None):
     """``t`` is a tensor of ``like``'s shape and device (and dtype, unless another is given), the last dimension
     contiguous."""
+    dtype = dtype or like.dtype
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == like.shape and t.stride(-1) == 1
+            and t.device == like.device):
+        return t
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device} (the inputs' device), not {t.device}")
-    if t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != like.shape:
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, not {tuple(t.shape)}")
     return _last_contiguous(t, name)
@@ -103,7 +107,7 @@ def _call(name, device, *args):
     else:
         with torch.cuda.device(device):
             rc = fn(*args)
-    if rc != 0:
+    if rc:
         raise RetentionError(name, rc)
 
 

@@ -31,6 +31,7 @@ struct Sequences {
 // tile and channel, what the tile passes on (recurrence.hip). Lanes take `vec`
 // channels, 16 bytes of them, or one where the whole row is shorter.
 constexpr int kScanChannels = 64;
+constexpr uint32_t kXcds = 8, kXcdUnits = 9;
 constexpr int kScanMaxWaves = 8;
 constexpr int kScanRows = 32;         // of a wave
 constexpr int kScanSigmoidBackRows = 16;  // of a wave of the sigmoid form's backward
@@ -57,11 +58,24 @@ struct ScanPlan {
 // The sigmoid form's backward reads four tensors; waves of 16 tokens let it
 // hold them in 128 registers, four waves to a SIMD: 605 us against 705 with 32
 // at 8 x 8192 x 4096.
+// Workgroups that start for n units of one tile: rounded up where they are
+// shared out among the XCDs in runs.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline uint32_t scan_round(uint32_t n) {
+  return n % kXcds && n < kXcdUnits ? n : (n + kXcds - 1) / kXcds * kXcds;
+}
 inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, int dtype, bool backward, int form) {
   ScanPlan p{};
   p.vec = dtype == 0 ? 4 : 8;
   if (d < p.vec) p.vec = 1;
-  p.units = static_cast<int64_t>(S) * H * ((d + kScanChannels - 1) / kScanChannels);
+  const int64_t columns = static_cast<int64_t>(H) * ((d + kScanChannels - 1) / kScanChannels);
+  if (columns > (int64_t{1} << 30)) {
+    p.blocks = columns;  // beyond any launch, and the products below
+    return p;
+  }
+  p.units = S * columns;
   p.wave_rows = p.vec == 1 ? kScanNarrowRows : backward && form == 0 ? kScanSigmoidBackRows : kScanRows;
   const int64_t many = backward && form != 0 ? 16 : 256;
   const int64_t most = p.units >= many ? kScanMaxWaves / 2 : kScanMaxWaves;
@@ -69,9 +83,13 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
   p.waves = static_cast<int>(waves < most ? waves : most);
   p.rows = p.waves * p.wave_rows;
   p.tiles = (static_cast<int64_t>(max_len) + p.rows - 1) / p.rows;
-  const int64_t columns = p.units / S;
   p.slots = packed && p.tiles > 1 ? N / p.rows + S : p.tiles * S;
-  p.blocks = p.units > (int64_t{1} << 40) ? p.units : columns * p.slots;
+  const int64_t together = packed && p.tiles > 1 ? columns : p.units;
+  if (together > (int64_t{1} << 30)) {
+    p.blocks = together;
+    return p;
+  }
+  p.blocks = int64_t{scan_round(static_cast<uint32_t>(together))} * (columns * p.slots / together);
   if (p.tiles > 1)
     p.bytes = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
               static_cast<size_t>(columns) * p.slots * kScanChannels * (sizeof(uint64_t) + sizeof(uint32_t));

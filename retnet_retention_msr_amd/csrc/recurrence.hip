@@ -37,7 +37,6 @@ namespace ret {
 
 namespace {
 
-constexpr uint32_t kXcds = 8;
 
 struct Piece {
   int64_t first;  // its first token in the row
@@ -192,16 +191,27 @@ struct ScanLane {
 };
 
 // The unit of this workgroup and the tile its number suggests. Workgroups go
-// round the eight XCDs; neighbouring slabs go to one of them where they can be
-// shared out evenly, so that the pieces of a row meet in one L2: 10 to 12%
-// faster at 8 x 8192 x 4096.
+// round the eight XCDs. Each XCD takes a run of neighbouring slabs, so that the
+// pieces of a row meet in one L2 (10 to 12% faster at 8 x 8192 x 4096), and
+// keeps them, so that the words between a unit's tiles stay near (runs that
+// moved on with the tiles: 27 us against 21 at 32768 x 256). Of n units the
+// runs are floor or ceil(n / 8) long, and a workgroup past the end of its run
+// has nothing to do; below kXcdUnits, where the longest run would hold up the
+// rest, the units go round one by one instead.
 struct ScanPlace {
   int64_t unit, sh, slot0;  // slot0: of the unit's tile 0, over all columns
   int h, slab, tile;
   Piece piece;
 };
-__device__ __forceinline__ uint32_t side_by_side(uint32_t i, uint32_t n) {
-  return n % kXcds ? i : i % kXcds * (n / kXcds) + i / kXcds;
+__device__ __forceinline__ bool side_by_side(uint32_t n, uint32_t& i, int& tile) {
+  const uint32_t round = scan_round(n);
+  tile = blockIdx.x / round;
+  i = blockIdx.x % round;
+  if (n % kXcds && n < kXcdUnits) return true;
+  const uint32_t run = i % kXcds;
+  auto begin = [&](uint32_t r) { return n / kXcds * r + n % kXcds * r / kXcds; };  // floor(r n / 8)
+  i = begin(run) + i / kXcds;
+  return i < begin(run + 1);
 }
 // First slot of packed sequence s; it grows with s, by at least the sequence's
 // tiles and at least 1.
@@ -211,7 +221,7 @@ __device__ __forceinline__ int first_slot(const Sequences& q, int s, int rows) {
 }
 __device__ __forceinline__ ScanPlace scan_place(const Sequences& q, uint32_t units, int tiles, int rows,
                                                 const ScanWords& w) {
-  ScanPlace p;
+  ScanPlace p{};
   const uint32_t slabs = (q.d + kScanChannels - 1) / kScanChannels, columns = q.H * slabs;
   int s;
   uint32_t column;
@@ -219,8 +229,12 @@ __device__ __forceinline__ ScanPlace scan_place(const Sequences& q, uint32_t uni
     // Tile after tile along the packed row, the columns of each together. The
     // last sequence whose first slot is not past this one, 64 lanes looking at
     // a time.
-    column = side_by_side(blockIdx.x % columns, columns);
-    const int slot = blockIdx.x / columns, lane = threadIdx.x & 63;
+    int slot;
+    if (!side_by_side(columns, column, slot)) {
+      p.tile = -1;
+      return p;
+    }
+    const int lane = threadIdx.x & 63;
     s = 0;
     int left = q.S;  // sequences s .. s + left - 1 are in question
     while (left > 1) {
@@ -238,8 +252,11 @@ __device__ __forceinline__ ScanPlace scan_place(const Sequences& q, uint32_t uni
   } else {
     // The units of one tile of tokens together, so that most tiles at work
     // belong to different ones.
-    const uint32_t unit = side_by_side(blockIdx.x % units, units);
-    p.tile = blockIdx.x / units;
+    uint32_t unit;
+    if (!side_by_side(units, unit, p.tile)) {
+      p.tile = -1;
+      return p;
+    }
     s = unit / columns;
     column = unit - s * columns;
     p.slot0 = column * w.slots + static_cast<int64_t>(s) * tiles;
@@ -349,6 +366,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   typedef Pack<T, V> P;
   const int rows = static_cast<int>(blockDim.x >> 6) * E;
   ScanPlace p = scan_place(q, units, tiles, rows, w);
+  if (p.tile < 0) return;
   const ScanLane<V> at(p.slab, q.d);
   const int len = p.piece.len;
   const T* xr = row_of<T>(x, p.piece.b, p.h) + p.piece.first * x.sn;
@@ -381,7 +399,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   // are left as the sequence has tiles. The loads start for the suggested tile
   // while the ticket is on its way. An empty sequence's tile 0 passes its
   // state on.
-  if (p.tile < 0 || (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len)) return;
+  if (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len) return;
   if (len > 0) load(p.tile);
   if (tiles > 1) {
     const int tile = take_ticket(w, p.unit, shared.tile);
@@ -469,6 +487,7 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   typedef Pack<T, V> P;
   const int rows = static_cast<int>(blockDim.x >> 6) * E;
   ScanPlace p = scan_place(q, units, tiles, rows, w);
+  if (p.tile < 0) return;
   const ScanLane<V> at(p.slab, q.d);
   const int len = p.piece.len;
   auto row = [&](const View& v) { return row_of<T>(v, p.piece.b, p.h) + p.piece.first * v.sn; };
@@ -503,7 +522,7 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
       }
     }
   };
-  if (p.tile < 0 || (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len)) return;
+  if (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len) return;
   if (len > 0) load(p.tile);
   if (tiles > 1) {
     const int tile = take_ticket(w, p.unit, shared.tile);
@@ -743,12 +762,14 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
   const hipError_t e = scan_words(p, workspace, &words, stream);
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
-  // Rows that do not begin on 16 bytes: the pieces that two workgroups write
-  // meet within cache lines, and two results of them fare better through the
-  // caches (4 x 7501 x 1001: bf16 111 us against 131, fp32 190 against 203; the
-  // forward's one result does not, 55 against 50).
+  // Rows that do not all begin on a cache line: the pieces that two workgroups
+  // write meet within lines, and two results of them fare better through the
+  // caches (bf16: 4 x 7501 x 1001 111 us against 131, 55 x 193 x 3824 108
+  // against 132, 10749 x 2728 105 against 108; fp32: 4 x 7501 x 1001 190
+  // against 203, 4 x 19454 x 696 321 against 313). The forward's one result
+  // mostly does not: 55 against 50 and 53 against 47 at the first and third.
   const int64_t size = dtype == 0 ? 4 : 2;
-  const bool cached = grad_x.sn * size % 16 != 0 || grad_gate.sn * size % 16 != 0;
+  const bool cached = grad_x.sn * size % 128 != 0 || grad_gate.sn * size % 128 != 0;
 #define RET_SCAN(T, FORM, V, E, CACHED)                                                                    \
   recurrence_backward_kernel<T, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(                           \
       grad_h, x, gate, h, grad_x, grad_gate, q, state_in, grad_state_out, grad_state_in, words,            \

@@ -120,6 +120,8 @@ def test_recurrence_refuses(lib, kw):
 def test_recurrence_limits(lib):
     assert recurrence(lib, B=1 << 16, H=1 << 10, N=1 << 10) == UNSUPPORTED
     assert recurrence(lib, d=(1 << 20) + 1) == UNSUPPORTED
+    assert recurrence(lib, B=1, H=(1 << 31) - 2, N=1, d=1 << 20, cu=A[5], S=1 << 20, strides=(0, 0, 0), h_strides=(0, 1 << 20, 0)) == UNSUPPORTED
+    assert recurrence(lib, B=1, cu=A[5], S=(1 << 20) + 1) == UNSUPPORTED
     assert recurrence(lib, strides=(1 << 34, 1 << 32, 1 << 24), h_strides=(19200, 6400, 64)) == UNSUPPORTED
     assert recurrence(lib, strides=(1 << 60, 6400, 64), h_strides=(19200, 6400, 64)) == UNSUPPORTED
 
