@@ -44,8 +44,9 @@ class Norm:
 NormLike = Union[Norm, GroupNorm]
 
 # torch's current stream as a number, without building a Stream object (2 us a
-# call, a fifth of a decode step's whole host time).
+# call, a fifth of a decode step's whole host time), and the current device.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(t):
@@ -102,7 +103,7 @@ def _ptr(t):
 def _call(name, device, *args):
     """Calls the entry point with ``device`` current; the stream is the last argument."""
     fn = getattr(_lib.load(), name)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -411,9 +412,10 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
     if scale is not None:
         _require(scale, "scale", (D,), torch.float32, dev)
     out, residual_out = _output(out, "out", x), _output(residual_out, "residual_out", x, stream)
-    for name, t in (("residual", residual), ("out", out), ("residual_out", residual_out)):
-        _rows_layout(t, name)
     _same(residual, "residual", x, stream)
+    if x.dim() > 3:
+        for name, t in (("residual", residual), ("out", out), ("residual_out", residual_out)):
+            _rows_layout(t, name)
     _call("retention_residual_norm", dev, _row_view(x), _row_view(residual), _row_view(out), _row_view(residual_out),
           *_row_dims(x), dt, _lib.RET_F32 if stream == torch.float32 else dt, n, _ptr(scale), float(alpha), _stream(x))
     return out, residual_out

@@ -40,6 +40,7 @@ struct ScanPlan {
   int vec, waves, wave_rows, rows;
   int64_t units, tiles;  // tiles of the longest sequence
   int64_t slots;         // tiles of a slab over all sequences: the workspace's places
+  bool folds;            // whether tiles pass on their folds too, or their states alone
   int64_t blocks;        // workgroups of the launch
   size_t bytes;          // workspace
 };
@@ -55,6 +56,10 @@ struct ScanPlan {
 // units (4 x 8192 x 4096) 153 and 152, 32 units (65536 x 2048) 186 and 174, 4
 // units (32768 x 256) 29 and 21. Backward, log form: 256 units 257 and 311, 32
 // units 294 and 362, 1 unit (65536 x 64) 37 and 24.
+// With many units a tile waits for its predecessor's state alone: it is mostly
+// there, and the folds' words would have to be filled, written and read (2% at
+// 8 x 8192 x 4096).
+constexpr int64_t kScanManyUnits = 256;
 // The sigmoid form's backward reads four tensors; waves of 16 tokens let it
 // hold them in 128 registers, four waves to a SIMD: 605 us against 705 with 32
 // at 8 x 8192 x 4096.
@@ -77,7 +82,7 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
   }
   p.units = S * columns;
   p.wave_rows = p.vec == 1 ? kScanNarrowRows : backward && form == 0 ? kScanSigmoidBackRows : kScanRows;
-  const int64_t many = backward && form != 0 ? 16 : 256;
+  const int64_t many = backward && form != 0 ? 16 : kScanManyUnits;
   const int64_t most = p.units >= many ? kScanMaxWaves / 2 : kScanMaxWaves;
   const int64_t waves = (static_cast<int64_t>(max_len) + p.wave_rows - 1) / p.wave_rows;
   p.waves = static_cast<int>(waves < most ? waves : most);
@@ -90,9 +95,10 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
     return p;
   }
   p.blocks = int64_t{scan_round(static_cast<uint32_t>(together))} * (columns * p.slots / together);
+  p.folds = packed || p.units < kScanManyUnits;
   if (p.tiles > 1)
     p.bytes = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
-              static_cast<size_t>(columns) * p.slots * kScanChannels * (sizeof(uint64_t) + sizeof(uint32_t));
+              static_cast<size_t>(columns) * p.slots * kScanChannels * (p.folds ? 12 : 4);
   return p;
 }
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,

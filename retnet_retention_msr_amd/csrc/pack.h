@@ -30,7 +30,11 @@ struct Pack<float, V> {
     return r;
   }
   static __device__ __forceinline__ void store(float* p, const float (&x)[V]) {
-    __builtin_nontemporal_store(pack(x), reinterpret_cast<anywhere*>(p));
+    // Eight floats are two accesses, each of which fills half of the lines it
+    // touches: these go through the caches (residual norm backward with an
+    // fp32 stream, 16384 x 4096: 235 us against 247).
+    if constexpr (V == 8) keep(p, x);
+    else __builtin_nontemporal_store(pack(x), reinterpret_cast<anywhere*>(p));
   }
   static __device__ __forceinline__ void keep(float* p, const float (&x)[V]) {
     *reinterpret_cast<anywhere*>(p) = pack(x);

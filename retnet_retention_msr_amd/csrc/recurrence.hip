@@ -71,8 +71,8 @@ __device__ __forceinline__ void gate_of(float g, float& a, float& c) {
 // floor(first token / rows) + s + tile, which no two of them share.
 struct ScanWords {
   uint32_t* ticket;  // [units], from all ones up
-  uint64_t* fold;    // [columns][slots][64]: Y, A
   uint32_t* state;   // [columns][slots][64]: the state after the tile
+  uint64_t* fold;    // [columns][slots][64]: Y, A; null: states alone
   int64_t slots;
 };
 
@@ -157,6 +157,18 @@ __device__ __forceinline__ float look_back(const uint64_t* fold, const uint32_t*
       break;
   }
   return y;
+}
+
+// The same from the last tile's state alone.
+__device__ __forceinline__ float last_state(const uint32_t* state, int tile) {
+  uint32_t s = ~0u;
+  for (int poll = 0; poll < kPolls; ++poll) {
+    s = __hip_atomic_load(state + static_cast<int64_t>(tile - 1) * kScanChannels, __ATOMIC_RELAXED,
+                          __HIP_MEMORY_SCOPE_AGENT);
+    if (__all(s != ~0u)) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  return __uint_as_float(s);  // all ones, a NaN, where it never came
 }
 
 // What a workgroup shares. Channel i of the slab is fold[wave][kPad + i]; the
@@ -324,8 +336,12 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&Y)[V], float (
     if (p.tile == 0) {
       carry = first && lane < left ? first[lane] : 0.0f;
     } else {
-      if (!end) publish(w.fold + here, TA, TY);
-      carry = look_back(w.fold + word, w.state + word, p.tile, shared.stash, lane);
+      if (w.fold) {
+        if (!end) publish(w.fold + here, TA, TY);
+        carry = look_back(w.fold + word, w.state + word, p.tile, shared.stash, lane);
+      } else {
+        carry = last_state(w.state + word, p.tile);
+      }
     }
     const float after = fmaf(TA, carry, TY);
     if (!end) publish(w.state + here, after);
@@ -712,8 +728,9 @@ hipError_t scan_words(const ScanPlan& p, void* workspace, ScanWords* words, hipS
   char* base = static_cast<char*>(workspace);
   words->ticket = reinterpret_cast<uint32_t*>(base);
   base += (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256;
-  words->fold = reinterpret_cast<uint64_t*>(base);
-  words->state = reinterpret_cast<uint32_t*>(base + (p.bytes - static_cast<size_t>(base - static_cast<char*>(workspace))) / 3 * 2);
+  words->state = reinterpret_cast<uint32_t*>(base);
+  const size_t states = (p.bytes - static_cast<size_t>(base - static_cast<char*>(workspace))) / (p.folds ? 3 : 1);
+  if (p.folds) words->fold = reinterpret_cast<uint64_t*>(base + states);
   words->slots = p.slots;
   const int64_t n = static_cast<int64_t>(p.bytes / sizeof(uint64_t));
   const int64_t blocks = (n + 255) / 256;

@@ -380,41 +380,39 @@ gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, in
         part, sums, partial + (static_cast<int64_t>(h) * gridDim.x + blockIdx.x) * kGatedNormSums * d, d, wanted);
 }
 
-// out[k][head * d + c] = sum over parts of partial[head][part][k][c]: 16
-// columns to a workgroup, 16 threads a column, joined in a fixed order. Grid
-// (columns / 16, sums).
+// out[k][head * d + c] = sum over parts of partial[head][part][k][c]: 32
+// columns (a cache line) of a head to a workgroup, 8 threads a column, joined
+// in a fixed order. Grid (columns / 32, sums, heads).
 __global__ void __launch_bounds__(kThreads)
-param_sum_kernel(const float* partial, int heads, int parts, int sums, int d, float* out0, float* out1, float* out2) {
-  __shared__ float all[16][17];
-  const int k = blockIdx.y;
+param_sum_kernel(const float* partial, int parts, int sums, int d, float* out0, float* out1, float* out2) {
+  constexpr int kCols = 32, kLots = kThreads / kCols;
+  __shared__ float all[kLots][kCols];
+  const int k = blockIdx.y, head = blockIdx.z;
   float* out = k == 0 ? out0 : k == 1 ? out1 : out2;
   if (!out) return;
-  const int64_t n = static_cast<int64_t>(heads) * d;
-  const int col = threadIdx.x & 15, lot = threadIdx.x >> 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + col;
+  const int col = threadIdx.x % kCols, lot = threadIdx.x / kCols;
+  const int c = blockIdx.x * kCols + col;
   float s = 0.0f;
-  if (i < n) {
-    const int64_t head = i / d;
-    const float* p = partial + ((head * parts) * sums + k) * d + (i - head * d);
+  if (c < d) {
     const int64_t stride = static_cast<int64_t>(sums) * d;
-#pragma unroll 8
-    for (int q = lot; q < parts; q += 16) s += p[q * stride];
+    const float* p = partial + (static_cast<int64_t>(head) * parts * sums + k) * d + c;
+#pragma unroll 16
+    for (int q = lot; q < parts; q += kLots) s += p[q * stride];
   }
   all[lot][col] = s;
   __syncthreads();
-  if (lot == 0 && i < n) {
+  if (lot == 0 && c < d) {
     s = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) s += all[q][col];
-    out[i] = s;
+    for (int q = 0; q < kLots; ++q) s += all[q][col];
+    out[static_cast<int64_t>(head) * d + c] = s;
   }
 }
 
 hipError_t sum_params(const float* partial, int heads, int parts, int sums, int d, float* out0, float* out1,
                       float* out2, hipStream_t stream) {
-  const int64_t n = static_cast<int64_t>(heads) * d;
-  param_sum_kernel<<<dim3(static_cast<unsigned>((n + 15) / 16), sums), kThreads, 0, stream>>>(partial, heads, parts,
-                                                                                             sums, d, out0, out1, out2);
+  param_sum_kernel<<<dim3((d + 31) / 32, sums, heads), kThreads, 0, stream>>>(partial, parts, sums, d, out0, out1,
+                                                                              out2);
   return hipGetLastError();
 }
 
@@ -492,7 +490,7 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
 
 // The row is r or, with `residual`, formed again from it and x.
 template <typename T, typename TR, int L, int V, int K, bool MASK>
-__global__ void __launch_bounds__(threads_of(L), V* K <= 8 || L == 1024 ? 4 : 2)
+__global__ void __launch_bounds__(threads_of(L), (sizeof(T) == 2 && V * K <= 8) || L == 1024 ? 4 : 2)
 residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, View dx, View dres, int rows, int N,
                               int D, NormArgs n, const float* scale, float alpha, float* partial, uint32_t wanted) {
   constexpr int E = V * K, G = threads_of(L) / L;
