@@ -494,7 +494,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then.
 template <typename T, int FORM, int V, int E, bool CACHED>
-__global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 ? 4 : 2)
+__global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(T) == 2 ? 4 : 2)
 recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
                            const float* state_in, const float* grad_state_out, float* grad_state_in, ScanWords w,
                            uint32_t units, int tiles) {
