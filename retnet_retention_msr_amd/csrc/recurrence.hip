@@ -202,7 +202,7 @@ struct ScanLane {
   }
 };
 
-// The unit of this workgroup and the tile its number suggests. Workgroups go
+// The unit of this workgroup and the tile its number stands for. Workgroups go
 // round the eight XCDs. Each XCD takes a run of neighbouring slabs, so that the
 // pieces of a row meet in one L2 (10 to 12% faster at 8 x 8192 x 4096), and
 // keeps them, so that the words between a unit's tiles stay near (runs that
@@ -411,19 +411,20 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
       }
     }
   };
-  // A workgroup whose suggestion lies past the end takes no ticket: as many
-  // are left as the sequence has tiles. The loads start for the suggested tile
-  // while the ticket is on its way. An empty sequence's tile 0 passes its
-  // state on.
+  // A workgroup whose number stands for a tile past the end takes no ticket: as
+  // many are left as the sequence has tiles. An empty sequence's tile 0 passes
+  // its state on. With many units the loads start for the tile of the
+  // workgroup's number while the ticket is on its way (backward at 8 x 8192 x
+  // 4096: 600 us against 700); with few, where tickets of neighbouring tiles
+  // cross and such loads are lost, they wait for it (backward of 4 x 7501 x
+  // 1001 fp32: 168 us against 190).
   if (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len) return;
-  if (len > 0) load(p.tile);
+  if (len > 0 && !w.fold) load(p.tile);
   if (tiles > 1) {
     const int tile = take_ticket(w, p.unit, shared.tile);
     if (tile > 0 && static_cast<int64_t>(tile) * rows >= len) return;
-    if (tile != p.tile) {
-      p.tile = tile;
-      load(tile);
-    }
+    if (w.fold ? len > 0 : tile != p.tile) load(tile);
+    p.tile = tile;
   }
   const int64_t row0 = static_cast<int64_t>(p.tile) * rows;
   const int64_t t0 = row0 + at.wave * E + at.sub * R;
@@ -539,14 +540,12 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
     }
   };
   if (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len) return;
-  if (len > 0) load(p.tile);
+  if (len > 0 && !w.fold) load(p.tile);
   if (tiles > 1) {
     const int tile = take_ticket(w, p.unit, shared.tile);
     if (tile > 0 && static_cast<int64_t>(tile) * rows >= len) return;
-    if (tile != p.tile) {
-      p.tile = tile;
-      load(tile);
-    }
+    if (w.fold ? len > 0 : tile != p.tile) load(tile);
+    p.tile = tile;
   }
   const int64_t row0 = static_cast<int64_t>(p.tile) * rows;
   const int64_t t0 = row0 + at.wave * E + at.sub * R;
