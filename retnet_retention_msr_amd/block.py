@@ -24,10 +24,10 @@ from typing import Optional, Union
 
 import torch
 
-from . import GroupNorm, RetentionError, _dtype_code, _lib, _require, _require_workspace
-from . import _stream as _stream_of
+from . import GroupNorm, RetentionError, _lib, _require, _require_workspace, _stream
 
 FORMS = {"sigmoid": 0, "log": 1}
+_CODES = {torch.float32: _lib.RET_F32, torch.bfloat16: _lib.RET_BF16}
 
 
 @dataclass
@@ -43,25 +43,29 @@ class Norm:
 
 NormLike = Union[Norm, GroupNorm]
 
-# torch's current stream as a number, without building a Stream object (2 us a
-# call, a fifth of a decode step's whole host time), and the current device.
+# A decode step's call is bound by the host, so what is checked for every
+# tensor is checked in one pass, and said in full only where it fails. torch's
+# current stream is asked for as a number: a Stream object costs 2 us, a fifth
+# of a step's whole host time.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(t):
-    return _stream_of(t) if _raw_stream is None else _raw_stream(t.device.index)
-
-
 def _activations(t, name, dims):
-    """``t`` is a device tensor with one of ``dims`` dimensions, the last contiguous."""
+    """``t`` is a device tensor of a supported dtype with one of ``dims`` dimensions, the last contiguous. Returns the
+    dtype's code."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() not in dims:
         raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, not {t.dim()}")
-    return _last_contiguous(t, name)
+    if t.stride(-1) != 1:
+        _last_contiguous(t, name)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
+    return code
 
 
 def _last_contiguous(t, name):
@@ -88,6 +92,14 @@ def _same(t, name, like, dtype=None):
     return _last_contiguous(t, name)
 
 
+def _f32(t, name, shape, device):
+    """``t`` is a contiguous float32 tensor of this shape on ``device``."""
+    if (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t
+    return _require(t, name, shape, torch.float32, device)
+
+
 def _new(like, dtype=None):
     return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
@@ -100,14 +112,24 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(name, device, *args):
-    """Calls the entry point with ``device`` current; the stream is the last argument."""
-    fn = getattr(_lib.load(), name)
-    if device.index == _current_device():
-        rc = fn(*args)
+def _view(t):
+    """The retention_view_t of a tensor of two to four dimensions: [B, H, N, d], or without the H, the N or both. The
+    strides of the dimensions that are missing are those of sizes of 1, which are not read."""
+    if t is None:
+        return None
+    s = t.stride()
+    return _lib.View(t.data_ptr(), s[0], s[1], s[-2])
+
+
+def _call(name, like, *args):
+    """Calls the entry point with ``like``'s device current, on its current stream."""
+    fn, device = getattr(_lib.load(), name), like.get_device()
+    stream = _stream(like) if _raw_stream is None else _raw_stream(device)
+    if device == _current_device():
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args)
+            rc = fn(*args, stream)
     if rc:
         raise RetentionError(name, rc)
 
@@ -127,14 +149,6 @@ def _form(form):
     if form not in FORMS:
         raise ValueError(f"form must be one of {sorted(FORMS)}, not {form!r}")
     return FORMS[form]
-
-
-def _seq_view(t):
-    """[B, N, D] (one head) or [B, H, N, d]."""
-    if t is None:
-        return None
-    s = t.stride()
-    return _lib.View(t.data_ptr(), s[0], 0, s[1]) if t.dim() == 3 else _lib.View(t.data_ptr(), s[0], s[1], s[2])
 
 
 def _sequences(t, cu_seqlens, max_len):
@@ -162,7 +176,7 @@ def _state_to_fill(t, name, shape, device):
         return torch.empty(shape, dtype=torch.float32, device=device)
     if t is False or t is None:
         return None
-    return _require(t, name, shape, torch.float32, device)
+    return _f32(t, name, shape, device)
 
 
 def gated_recurrence_workspace_bytes(sequences, H, N, d, dtype=torch.bfloat16, max_len=None) -> int:
@@ -193,19 +207,19 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     outside every sequence, or beyond max_len of one, are not written, so in
     an output allocated here they are undefined.
     """
-    _activations(x, "x", (3, 4))
+    dt = _activations(x, "x", (3, 4))
     _same(gate, "gate", x)
-    code, dt = _form(form), _dtype_code(x)
+    code = _form(form)
     dims, states, S, max_len = _sequences(x, cu_seqlens, max_len)
     dev = x.device
     out = _output(out, "out", x)
     if state_in is not None:
-        _require(state_in, "state_in", states, torch.float32, dev)
+        _f32(state_in, "state_in", states, dev)
     state_out = _state_to_fill(state_out, "state_out", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence", dev, _seq_view(x), _seq_view(gate), _seq_view(out), *dims, code, dt,
-          _ptr(state_in), _ptr(state_out), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have, _stream(x))
+    _call("retention_gated_recurrence", x, _view(x), _view(gate), _view(out), *dims, code, dt, _ptr(state_in),
+          _ptr(state_out), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have)
     return out, state_out
 
 
@@ -222,14 +236,13 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
     gradient of a broadcast input comes in the input's full shape.
     """
     code = _form(form)
-    _activations(gate, "gate", (3, 4))
+    dt = _activations(gate, "gate", (3, 4))
     _same(grad_h, "grad_h", gate)
     _same(h, "h", gate)
     if x is not None:
         _same(x, "x", gate)
     elif code == 0:
         raise ValueError("the sigmoid form needs x")
-    dt = _dtype_code(gate)
     dims, states, S, max_len = _sequences(gate, cu_seqlens, max_len)
     dev = gate.device
     if grads is None:
@@ -240,20 +253,14 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
         _same(t, name, gate)
     for name, t in (("state_in", state_in), ("grad_state_out", grad_state_out)):
         if t is not None:
-            _require(t, name, states, torch.float32, dev)
+            _f32(t, name, states, dev)
     grad_state_in = _state_to_fill(grad_state_in, "grad_state_in", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence_backward", dev, _seq_view(grad_h), _seq_view(x), _seq_view(gate), _seq_view(h),
-          _seq_view(grads[0]), _seq_view(grads[1]), *dims, code, dt, _ptr(state_in), _ptr(grad_state_out),
-          _ptr(grad_state_in), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have, _stream(gate))
+    _call("retention_gated_recurrence_backward", gate, _view(grad_h), _view(x), _view(gate), _view(h),
+          _view(grads[0]), _view(grads[1]), *dims, code, dt, _ptr(state_in), _ptr(grad_state_out),
+          _ptr(grad_state_in), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have)
     return grads[0], grads[1], grad_state_in
-
-
-def _token_view(t):
-    """[B, D] (one head) or [B, H, d], one token each."""
-    s = t.stride()
-    return _lib.View(t.data_ptr(), s[0], s[1] if t.dim() == 3 else 0, 0)
 
 
 def gated_recurrence_step(x, gate, state, form: str = "sigmoid", slots=None, out=None):
@@ -265,20 +272,18 @@ def gated_recurrence_step(x, gate, state, form: str = "sigmoid", slots=None, out
     output is not written. Rows naming the same slot take effect one after
     another in row order.
     """
-    _activations(x, "x", (2, 3))
+    dt = _activations(x, "x", (2, 3))
     _same(gate, "gate", x)
-    code, dt = _form(form), _dtype_code(x)
-    B, d, dev = x.size(0), x.size(-1), x.device
-    H = x.size(1) if x.dim() == 3 else 1
-    if not isinstance(state, torch.Tensor) or state.dim() != x.dim():
-        raise ValueError(f"state must be a tensor with {x.dim()} dimensions")
-    P = state.size(0)
-    _require(state, "state", (B if slots is None else P, *x.shape[1:]), torch.float32, dev)
+    code, dev, shape = _form(form), x.device, x.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != len(shape):
+        raise ValueError(f"state must be a tensor with {len(shape)} dimensions")
+    P = shape[0] if slots is None else state.size(0)
+    _f32(state, "state", (P, *shape[1:]), dev)
     if slots is not None:
-        _require(slots, "slots", (B,), torch.int32, dev)
+        _require(slots, "slots", shape[:1], torch.int32, dev)
     out = _output(out, "out", x)
-    _call("retention_gated_recurrence_step", dev, _token_view(x), _token_view(gate), _token_view(out), B, H, d, code,
-          dt, state.data_ptr(), P, _ptr(slots), _stream(x))
+    _call("retention_gated_recurrence_step", x, _view(x), _view(gate), _view(out), shape[0],
+          shape[1] if len(shape) == 3 else 1, shape[-1], code, dt, state.data_ptr(), P, _ptr(slots))
     return out
 
 
@@ -290,18 +295,12 @@ def _norm_struct(norm, n, device):
     """The retention_norm_t of ``norm`` with n weights and biases; its tensors stay alive in the caller's ``norm``."""
     if not isinstance(norm, (Norm, GroupNorm)):
         raise ValueError("norm must be a Norm or a GroupNorm")
-    for name, t in (("weight", norm.weight), ("bias", norm.bias)):
-        if t is not None:
-            _require(t, f"the norm's {name}", (n,), torch.float32, device)
-    return _lib.NormStruct(float(norm.eps), int(getattr(norm, "rms", False)), _ptr(norm.weight), _ptr(norm.bias))
-
-
-def _head_view(t):
-    """[B, H, N, d], or [B, H, d] for one token."""
-    if t is None:
-        return None
-    s = t.stride()
-    return _lib.View(t.data_ptr(), s[0], s[1], s[2] if t.dim() == 4 else 0)
+    weight, bias = norm.weight, norm.bias
+    if weight is not None:
+        weight = _f32(weight, "the norm's weight", (n,), device).data_ptr()
+    if bias is not None:
+        bias = _f32(bias, "the norm's bias", (n,), device).data_ptr()
+    return _lib.NormStruct(norm.eps, getattr(norm, "rms", False), weight, bias)
 
 
 def _head_dims(t):
@@ -317,13 +316,13 @@ def gated_norm(o, gate=None, norm: NormLike = GroupNorm(), out=None):
     contiguous tensors this is the ``gn``/``gate`` epilogue of ``chunkwise``
     as an operator of its own, for training, where the backward needs o.
     """
-    _activations(o, "o", (3, 4))
+    dt = _activations(o, "o", (3, 4))
     if gate is not None:
         _same(gate, "gate", o)
-    dims, dt = _head_dims(o), _dtype_code(o)
+    dims = _head_dims(o)
     n = _norm_struct(norm, dims[1] * dims[3], o.device)
     out = _output(out, "out", o)
-    _call("retention_gated_norm", o.device, _head_view(o), _head_view(gate), _head_view(out), *dims, dt, n, _stream(o))
+    _call("retention_gated_norm", o, _view(o), _view(gate), _view(out), *dims, dt, n)
     return out
 
 
@@ -336,11 +335,11 @@ def gated_norm_backward(grad_y, o, gate=None, norm: NormLike = GroupNorm(), grad
     """Gradients of gated_norm for dL/dy = grad_y. Returns (grad_o, grad_gate, grad_weight, grad_bias): grad_gate is
     None without a gate, grad_weight and grad_bias (fp32 [H*d]) where the norm has no weight or bias. ``grads``:
     optional preallocated (grad_o, grad_gate). grad_o is what chunkwise_backward takes as grad_o."""
-    _activations(o, "o", (3, 4))
+    dt = _activations(o, "o", (3, 4))
     _same(grad_y, "grad_y", o)
     if gate is not None:
         _same(gate, "gate", o)
-    dims, dt, dev = _head_dims(o), _dtype_code(o), o.device
+    dims, dev = _head_dims(o), o.device
     n = _norm_struct(norm, dims[1] * dims[3], dev)
     if grads is None:
         grads = (_new(o), None if gate is None else _new(o))
@@ -351,22 +350,17 @@ def gated_norm_backward(grad_y, o, gate=None, norm: NormLike = GroupNorm(), grad
         _same(grads[1], "grad_gate", o)
     dw = None if norm.weight is None else torch.empty_like(norm.weight)
     db = None if norm.bias is None else torch.empty_like(norm.bias)
-    nbytes = int(_lib.load().retention_gated_norm_backward_workspace_bytes(*dims, dt, int(bool(dw is not None or db is not None))))
+    params = dw is not None or db is not None
+    nbytes = _lib.load().retention_gated_norm_backward_workspace_bytes(*dims, dt, params) if params else 0
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_norm_backward", dev, _head_view(grad_y), _head_view(o), _head_view(gate),
-          _head_view(grads[0]), _head_view(grads[1]), *dims, dt, n, _ptr(dw), _ptr(db), _ptr(workspace), have,
-          _stream(o))
+    _call("retention_gated_norm_backward", o, _view(grad_y), _view(o), _view(gate), _view(grads[0]), _view(grads[1]),
+          *dims, dt, n, _ptr(dw), _ptr(db), _ptr(workspace), have)
     return grads[0], grads[1], dw, db
 
 
-def _row_view(t):
-    """Rows of the last dimension: [B, N, D] or fewer dimensions with any strides, or more of a contiguous tensor."""
-    if t is None:
-        return None
-    s = t.stride()
-    if t.dim() == 3:
-        return _lib.View(t.data_ptr(), s[0], 0, s[1])
-    return _lib.View(t.data_ptr(), 0, 0, s[0] if t.dim() == 2 else t.size(-1))
+def _rows_view(t):
+    """Rows of the last dimension: [B, N, D] or [R, D] with any strides, more dimensions of a contiguous tensor, or one."""
+    return _lib.View(t.data_ptr(), 0, 0, 0) if t is not None and t.dim() == 1 else _view(t)
 
 
 def _row_dims(t):
@@ -376,13 +370,9 @@ def _row_dims(t):
 
 
 def _rows(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() == 0:
-        raise ValueError(f"{name} must have a dimension to norm over")
-    return _rows_layout(_last_contiguous(t, name), name)
+    dt = _activations(t, name, range(1, 65))
+    _rows_layout(t, name)
+    return dt
 
 
 def _rows_layout(t, name):
@@ -405,19 +395,18 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
     dtype or float32, y has x's. ``scale`` (fp32 [D], default 1) weighs the
     branch per channel.
     """
-    _rows(x, "x")
-    dt, dev, D = _dtype_code(x), x.device, x.size(-1)
+    dt, dev, D = _rows(x, "x"), x.device, x.size(-1)
     stream = _stream_dtype(residual, "residual", x.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
-        _require(scale, "scale", (D,), torch.float32, dev)
+        _f32(scale, "scale", (D,), dev)
     out, residual_out = _output(out, "out", x), _output(residual_out, "residual_out", x, stream)
     _same(residual, "residual", x, stream)
     if x.dim() > 3:
         for name, t in (("residual", residual), ("out", out), ("residual_out", residual_out)):
             _rows_layout(t, name)
-    _call("retention_residual_norm", dev, _row_view(x), _row_view(residual), _row_view(out), _row_view(residual_out),
-          *_row_dims(x), dt, _lib.RET_F32 if stream == torch.float32 else dt, n, _ptr(scale), float(alpha), _stream(x))
+    _call("retention_residual_norm", x, _rows_view(x), _rows_view(residual), _rows_view(out), _rows_view(residual_out),
+          *_row_dims(x), dt, _CODES[stream], n, _ptr(scale), float(alpha))
     return out, residual_out
 
 
@@ -440,15 +429,14 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     and grad_x is grad_residual, the same tensor. ``grads``: optional
     preallocated (grad_x, grad_residual), two tensors.
     """
-    _rows(grad_y, "grad_y")
-    dt, dev, D = _dtype_code(grad_y), grad_y.device, grad_y.size(-1)
+    dt, dev, D = _rows(grad_y, "grad_y"), grad_y.device, grad_y.size(-1)
     if residual is not None and x is None:
         raise ValueError("residual needs x")
     row, name = (r, "r") if residual is None else (residual, "residual")
     stream = _stream_dtype(row, name, grad_y.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
-        _require(scale, "scale", (D,), torch.float32, dev)
+        _f32(scale, "scale", (D,), dev)
     if grads is None:
         d_res = _new(grad_y, stream)
         shared = scale is None and float(alpha) == 1.0 and stream == grad_y.dtype
@@ -469,12 +457,11 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     db = None if norm.bias is None else torch.empty_like(norm.bias)
     params = any(t is not None for t in (d_scale, dw, db))
     dims = _row_dims(grad_y)
-    nbytes = int(_lib.load().retention_residual_norm_backward_workspace_bytes(*dims, dt, int(params)))
+    nbytes = _lib.load().retention_residual_norm_backward_workspace_bytes(*dims, dt, params) if params else 0
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_residual_norm_backward", dev, _row_view(grad_y), _row_view(grad_r),
-          None if residual is not None else _row_view(r),
-          _row_view(x if d_scale is not None or residual is not None else None), _row_view(residual),
-          None if shared else _row_view(grads[0]), _row_view(grads[1]), *dims, dt,
-          _lib.RET_F32 if stream == torch.float32 else dt, n, _ptr(scale), float(alpha), _ptr(d_scale), _ptr(dw),
-          _ptr(db), _ptr(workspace), have, _stream(grad_y))
+    _call("retention_residual_norm_backward", grad_y, _rows_view(grad_y), _rows_view(grad_r),
+          None if residual is not None else _rows_view(r),
+          _rows_view(x if d_scale is not None or residual is not None else None), _rows_view(residual),
+          None if shared else _rows_view(grads[0]), _rows_view(grads[1]), *dims, dt,
+          _CODES[stream], n, _ptr(scale), float(alpha), _ptr(d_scale), _ptr(dw), _ptr(db), _ptr(workspace), have)
     return grads[0], grads[1], d_scale, dw, db

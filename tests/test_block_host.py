@@ -282,13 +282,33 @@ def test_same_checks_device_dtype_shape_and_layout(bad, match):
 
 def test_strided_views_are_taken_as_they_are():
     wide = torch.zeros(2, 8, 40)
-    v = block._seq_view(wide[..., 3:19])
-    assert (v.data, v.stride_b, v.stride_h, v.stride_n) == (wide.data_ptr() + 12, 320, 0, 40)
+    v = block._view(wide[..., 3:19])  # [B, N, D]: one head, whose stride is not read
+    assert (v.data, v.stride_b, v.stride_n) == (wide.data_ptr() + 12, 320, 40)
     t = torch.zeros(2, 8, 3, 16).transpose(1, 2)  # [B, H, N, d] of a token-major tensor
-    v = block._head_view(t)
+    v = block._view(t)
     assert (v.stride_b, v.stride_h, v.stride_n) == (8 * 48, 16, 48)
-    v = block._row_view(torch.zeros(2, 3, 4, 16))
+    v = block._view(t[:, :, 0])  # [B, H, d]: one token
+    assert (v.stride_b, v.stride_h) == (8 * 48, 16)
+    v = block._view(wide[:, 0])  # [B, D]
+    assert v.stride_b == 320
+    v = block._rows_view(torch.zeros(2, 3, 4, 16))
     assert v.stride_n == 16 and block._row_dims(torch.zeros(2, 3, 4, 16)) == (1, 24, 16)
+    v = block._rows_view(wide[0])  # [R, D]
+    assert v.stride_n == 40 and block._row_dims(wide[0]) == (1, 8, 40)
+    assert block._row_dims(torch.zeros(16)) == (1, 1, 16)
+
+
+def test_unsupported_dtypes_are_type_errors():
+    class Device(torch.Tensor):  # a host tensor that says it is on the device: the dtype is looked at before any use
+        is_cuda = True
+
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        block._activations(torch.zeros(2, 8, 16, dtype=torch.float16).as_subclass(Device), "x", (3, 4))
+    assert block._activations(torch.zeros(2, 8, 16).as_subclass(Device), "x", (3, 4)) == _lib.RET_F32
+    with pytest.raises(ValueError, match="contiguous last dimension"):
+        block._activations(torch.zeros(2, 16, 8).transpose(1, 2).as_subclass(Device), "x", (3, 4))
+    with pytest.raises(ValueError, match="3 or 4 dimensions"):
+        block._activations(torch.zeros(8, 16).as_subclass(Device), "x", (3, 4))
 
 
 def test_sequence_arguments(no_library):
