@@ -75,7 +75,8 @@ SHAPES = [
     ((2, 256, 128), "log", F32), ((1, 257, 64), "log", BF16), ((1, 511, 33), "sigmoid", BF16),
     ((1, 513, 16), "sigmoid", F32), ((3, 1000, 200), "sigmoid", BF16), ((1, 2049, 70), "log", BF16),
     ((1, 5000, 64), "sigmoid", BF16), ((1, 4097, 8), "log", F32), ((2, 3, 77, 24), "sigmoid", BF16),
-    ((1, 16, 700, 64), "log", BF16), ((2, 5, 300, 7), "sigmoid", F32),
+    ((1, 16, 700, 64), "log", BF16), ((2, 5, 300, 7), "sigmoid", F32), ((1, 700, 5), "log", BF16), ((2, 500, 3), "sigmoid", F32),
+    ((260, 270, 64), "sigmoid", BF16), ((87, 3, 400, 24), "log", F32),
 ]
 
 
@@ -261,6 +262,69 @@ def test_broadcast_gate():
     _, dg, _ = ret.gated_recurrence_backward(dh, x, g1.expand(shape), h, "sigmoid")
     _, ref, _ = ret.gated_recurrence_backward(dh, x, g1.expand(shape).contiguous(), h, "sigmoid")
     assert dg.shape == shape and torch.equal(dg, ref)
+
+
+def test_nan_stays_with_its_channel_sequence_and_later_tokens():
+    """A NaN input reaches the tokens from its own on in its own channel, however they are cut into pieces, and nothing
+    else; its bits do not matter (all ones is what the library's own words hold before they are written)."""
+    _announce("nan")
+    B, N, D = 2, 3000, 72
+    x, g = _randn((B, N, D), 1), _gate((B, N, D), 2, F32, "log").clamp_(min=-5)
+    want, s_want = ret.gated_recurrence(x.to(DEV), g.to(DEV), "log", state_out=True)
+    bad = x.clone()
+    bad[1, 1000, 7] = torch.tensor(-1, dtype=torch.int32).view(F32)
+    h, s = ret.gated_recurrence(bad.to(DEV), g.to(DEV), "log", state_out=True)
+    hit = torch.zeros(B, N, D, dtype=torch.bool)
+    hit[1, 1000:, 7] = True
+    assert torch.equal(h.isnan().cpu(), hit) and torch.equal(h[~hit], want[~hit])
+    assert s.isnan().nonzero().tolist() == [[1, 7]]
+    dh = torch.zeros(B, N, D)
+    dh[1, 1000, 7] = float("nan")
+    dx, dg, ds = ret.gated_recurrence_backward(dh.to(DEV), x.to(DEV), g.to(DEV), want, "log", grad_state_in=True)
+    assert dx.isnan().nonzero().shape[0] == 1001 and bool(dx[1, :1001, 7].isnan().all())
+    assert ds.isnan().nonzero().tolist() == [[1, 7]] and bool((dx[0] == 0).all())
+
+
+def test_a_workspace_serves_any_contents_and_both_directions():
+    _announce("workspace")
+    for shape, form in (((1, 3000, 64), "sigmoid"), ((260, 300, 64), "log")):
+        x, g, dh = _randn(shape, 1).to(DEV), _gate(shape, 2, F32, form).to(DEV), _randn(shape, 3).to(DEV)
+        want = ret.gated_recurrence(x, g, form, state_out=True)
+        back = ret.gated_recurrence_backward(dh, x, g, want[0], form, grad_state_in=True)
+        n = ret.gated_recurrence_workspace_bytes(shape[0], 1, shape[1], shape[2], F32)
+        assert n > 0
+        for fill in (0, 255, 66):
+            ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+            for _ in range(2):  # the second call finds what the first one left
+                h, s = ret.gated_recurrence(x, g, form, state_out=True, workspace=ws)
+                assert torch.equal(h, want[0]) and torch.equal(s, want[1])
+                got = ret.gated_recurrence_backward(dh, x, g, h, form, grad_state_in=True, workspace=ws)
+                assert all(torch.equal(a, b) for a, b in zip(got, back))
+    with pytest.raises(ValueError, match="bytes are needed|are needed"):
+        ret.gated_recurrence(x, g, form, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+def test_refusals_reach_python_as_errors():
+    """What only the C ABI can tell comes back as RetentionError, and nothing is launched."""
+    _announce("refusals")
+    x = _randn((2, 40, 64), 1).to(DEV)
+    mark = x.clone()
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.gated_recurrence(x, mark, out=x)
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.gated_norm(x.view(2, 4, 10, 64), out=x.view(2, 4, 10, 64))
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.gated_recurrence(x, mark, out=torch.zeros(1, 40, 64, device=DEV).expand(2, 40, 64))
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.gated_recurrence_step(x[:, 0], x[:, 1], mark.view(-1)[:128].view(2, 64), out=mark.view(-1)[64:192].view(2, 64))
+    with pytest.raises(ret.RetentionError, match="unsupported"):
+        ret.gated_norm(torch.zeros(1, 1, 1, 2048, device=DEV))
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.residual_norm(x, x, ret.Norm(eps=float("nan")))
+    with pytest.raises(ret.RetentionError, match="invalid argument"):
+        ret.gated_recurrence(x[:, :0], x[:, :0])
+    torch.cuda.synchronize()
+    assert torch.equal(x, mark)
 
 
 def test_log_form_needs_no_x():
@@ -622,6 +686,29 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for k, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b), (i, k)
+
+
+def test_outputs_past_two_to_the_31_elements():
+    """A tensor of 2.2e9 values: the last rows of the outputs, against the oracle from the state the rows before leave
+    (the running mean of 0.5, to a rounding of fp32, which the oracle's bound counts per token) and against the same rows
+    on their own."""
+    _announce("2.2e9 values")
+    N, D, k = 34000, 65536, 40
+    x = torch.empty(1, N, D, dtype=BF16, device=DEV)
+    x.view(-1)[:].fill_(0.5)
+    x[:, -k:] = _randn((1, k, D), 1, BF16).to(DEV)
+    g = torch.zeros(1, 1, D, dtype=BF16, device=DEV).expand(1, N, D)
+    assert x.numel() > 2 ** 31
+    h, s = ret.gated_recurrence(x, g, state_out=True)
+    start = h[:, -k - 1].float()
+    assert bool((start == 0.5).all())
+    args = (x[:, -k:], g[:, -k:], "sigmoid", start)
+    (ref, end), (e, e_end) = orc.recurrence(*args), orc.recurrence_error(*args)
+    _check(h[:, -k:], ref, e, "h")
+    _check(s, end, e_end, "state")
+    y, _ = ret.residual_norm(x.view(-1, 16384), h.view(-1, 16384), ret.Norm(EPS, rms=True))
+    y2, _ = ret.residual_norm(x.view(-1, 16384)[-k:], h.view(-1, 16384)[-k:], ret.Norm(EPS, rms=True))
+    assert torch.equal(y[-k:], y2)
 
 
 def test_large_offsets():
