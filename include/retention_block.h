@@ -63,13 +63,14 @@ enum retention_gate_form {
  * cu_seqlens[s + 1] of the one row; max_len bounds the length of a sequence.
  * A sequence may be empty (its state passes through). Tokens outside every
  * sequence, or beyond max_len of one, are neither read nor written. Offsets
- * outside [0, N] are clamped into it. At most 2^20 sequences, d <= 2^20 and token strides (stride_n)
- * below 2^24 elements, else RET_ERR_UNSUPPORTED. Without cu_seqlens (NULL) `sequences`
- * must be B and max_len N.
+ * outside [0, N] are clamped into it. Without cu_seqlens (NULL) `sequences`
+ * must be B and max_len N. At most 2^20 sequences, d <= 2^20 and token strides
+ * (stride_n) below 2^24 elements, else RET_ERR_UNSUPPORTED.
  *
  * workspace: retention_gated_recurrence_workspace_bytes(...) bytes (packed:
- * whether there are cu_seqlens; the same for the backward), 8-byte aligned, its contents on entry do not matter; two calls that may overlap in time
- * need one each.
+ * whether there are cu_seqlens; the same for the backward), 8-byte aligned; its
+ * contents on entry do not matter. Calls that may overlap in time need one
+ * each.
  */
 size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int N, int max_len, int packed, int d,
                                                   int dtype);
@@ -177,9 +178,10 @@ size_t retention_residual_norm_backward_workspace_bytes(int B, int N, int D, int
 int retention_residual_norm_backward(const retention_view_t* grad_y, const retention_view_t* grad_r,
                                      const retention_view_t* r, const retention_view_t* x,
                                      const retention_view_t* residual, const retention_view_t* grad_x,
-                                     const retention_view_t* grad_residual, int B, int N, int D, int dtype, int stream_dtype, const retention_norm_t* norm,
-                                     const float* scale, float alpha, float* grad_scale, float* grad_weight,
-                                     float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+                                     const retention_view_t* grad_residual, int B, int N, int D, int dtype,
+                                     int stream_dtype, const retention_norm_t* norm, const float* scale, float alpha,
+                                     float* grad_scale, float* grad_weight, float* grad_bias, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

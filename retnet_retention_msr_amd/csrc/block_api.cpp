@@ -304,7 +304,8 @@ int retention_gated_norm(const retention_view_t* o, const retention_view_t* gate
 }
 
 size_t retention_gated_norm_backward_workspace_bytes(int B, int H, int N, int d, int dtype, int with_params) {
-  if (check_dims(B, H, N, d, dtype) != RET_OK || d > RETENTION_MAX_DV || H > RETENTION_MAX_HEADS || !with_params) return 0;
+  if (check_dims(B, H, N, d, dtype) != RET_OK || d > RETENTION_MAX_DV || H > RETENTION_MAX_HEADS || !with_params)
+    return 0;
   return ret::param_bytes(H, B * N, d, ret::kGatedNormSums, ret::kGatedBackGroups);
 }
 
@@ -423,8 +424,8 @@ int retention_residual_norm_backward(const retention_view_t* grad_y, const reten
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }
   if (ranges.clash()) return RET_ERR_INVALID_ARG;
-  return status_of(ret::launch_residual_norm_backward(dtype, stream_dtype, vdy, vdr, vr, vx, vres, vdx, vdres, B, N, D, n,
-                                                      scale, alpha, grad_scale, grad_weight, grad_bias, workspace,
+  return status_of(ret::launch_residual_norm_backward(dtype, stream_dtype, vdy, vdr, vr, vx, vres, vdx, vdres, B, N, D,
+                                                      n, scale, alpha, grad_scale, grad_weight, grad_bias, workspace,
                                                       static_cast<hipStream_t>(stream)));
 }
 
