@@ -359,8 +359,11 @@ def gated_norm_backward(grad_y, o, gate=None, norm: NormLike = GroupNorm(), grad
 
 
 def _rows_view(t):
-    """Rows of the last dimension: [B, N, D] or [R, D] with any strides, more dimensions of a contiguous tensor, or one."""
-    return _lib.View(t.data_ptr(), 0, 0, 0) if t is not None and t.dim() == 1 else _view(t)
+    """Rows of the last dimension: [B, N, D] or [R, D] with any strides, one, or those of a contiguous tensor of more
+    dimensions, which lie D apart (the stride of a dimension of one element says nothing)."""
+    if t is None or 2 <= t.dim() <= 3:
+        return _view(t)
+    return _lib.View(t.data_ptr(), 0, 0, t.size(-1))
 
 
 def _row_dims(t):

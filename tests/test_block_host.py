@@ -342,3 +342,10 @@ def test_norm_arguments():
 def test_the_epilogue_refuses_the_rms_form():
     with pytest.raises(ValueError, match="root-mean-square"):
         ret._gn_struct(ret.Norm(rms=True), 2, 8, torch.device("cpu"))
+
+
+def test_rows_of_many_dimensions_are_told_by_their_length():
+    """Contiguous is said whatever the stride of a dimension of one element: the rows of such a tensor are D apart."""
+    t = torch.zeros(2, 3, 1, 4, 16).transpose(2, 3)  # [2, 3, 4, 1, 16], 64 the stride of the 1
+    assert t.is_contiguous() and t.stride(-2) == 64
+    assert block._rows_view(block._rows_layout(t, "x")).stride_n == 16 and block._row_dims(t) == (1, 24, 16)

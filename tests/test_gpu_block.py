@@ -591,6 +591,19 @@ def test_constant_rows_and_huge_values():
     assert bool((dgate[::2] == 0).all()) and bool((dgate[1::2] == 1).all())
 
 
+def test_residual_norm_of_many_dimensions():
+    """Rows in five dimensions, one of them of one element with a stride of its own, are those of the flat tensor."""
+    _announce("residual norm in five dimensions")
+    norm = ret.Norm(EPS, _randn((64,), 1).to(DEV), rms=True)
+    x, res, dy = (_randn((2, 3, 1, 4, 64), i, BF16).to(DEV).transpose(2, 3) for i in (2, 3, 4))
+    assert x.is_contiguous() and x.stride(-2) != 64
+    flat = [t.reshape(24, 64) for t in (x, res, dy)]
+    for got, ref in zip(ret.residual_norm(x, res, norm), ret.residual_norm(flat[0], flat[1], norm)):
+        assert got.shape == x.shape and torch.equal(got.reshape(24, 64), ref)
+    for got, ref in zip(ret.residual_norm_backward(dy, res, norm), ret.residual_norm_backward(flat[2], flat[1], norm)):
+        assert got is ref is None or torch.equal(got.reshape(ref.shape), ref)
+
+
 # ---------------------------------------------------------------------------
 # Together
 
