@@ -65,7 +65,12 @@ enum retention_gate_form {
  * sequence, or beyond max_len of one, are neither read nor written. Offsets
  * outside [0, N] are clamped into it. Without cu_seqlens (NULL) `sequences`
  * must be B and max_len N. At most 2^20 sequences, d <= 2^20 and token strides
- * (stride_n) below 2^24 elements, else RET_ERR_UNSUPPORTED.
+ * (stride_n) below 2^24 elements, else RET_ERR_UNSUPPORTED, as beyond 2^32
+ * threads of a launch (2^26 pieces of 64 channels of a token, say).
+ *
+ * Gates above 0 in the log form are taken where the products of a channel's
+ * decays over up to 256 tokens stay within fp32's range: beyond it h may be inf
+ * or NaN where the formula's is finite.
  *
  * workspace: retention_gated_recurrence_workspace_bytes(...) bytes (packed:
  * whether there are cu_seqlens; the same for the backward), 8-byte aligned; its

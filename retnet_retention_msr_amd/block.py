@@ -100,6 +100,13 @@ def _f32(t, name, shape, device):
     return _require(t, name, shape, torch.float32, device)
 
 
+def _ints(*sizes):
+    """Sizes that reach the C library as ints."""
+    if max(sizes) >> 31:
+        raise ValueError(f"a size of {max(sizes)} is too large")
+    return sizes
+
+
 def _new(like, dtype=None):
     return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
@@ -165,10 +172,10 @@ def _sequences(t, cu_seqlens, max_len):
         _require(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, t.device)
         if B != 1:
             raise ValueError("packed sequences (cu_seqlens) need a batch of one row")
-        S, max_len = cu_seqlens.numel() - 1, N if max_len is None else int(max_len)
+        S, max_len = cu_seqlens.numel() - 1, N if max_len is None else min(int(max_len), N)
         if max_len <= 0:
             raise ValueError("max_len must be positive")
-    return (B, H, N, d), ((S, H, d) if t.dim() == 4 else (S, d)), S, max_len
+    return _ints(B, H, N, d), ((S, H, d) if t.dim() == 4 else (S, d)), S, max_len
 
 
 def _state_to_fill(t, name, shape, device):
@@ -197,7 +204,8 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
 
     ``form`` "sigmoid": a = sigmoid(gate), h_t = a_t h_{t-1} + (1 - a_t) x_t;
     "log": a = exp(gate), h_t = a_t h_{t-1} + x_t (gate <= 0 for a decay; -inf
-    starts the state anew). x and gate are [B, N, D] or [B, H, N, d]; states
+    starts the state anew; above 0 only while the products of 256 tokens' decays
+    stay in fp32's range). x and gate are [B, N, D] or [B, H, N, d]; states
     are fp32 [B, D] or [B, H, d]. ``state_out``: False (not produced), True
     (allocate) or a tensor to fill (it may be ``state_in`` itself).
 
@@ -263,6 +271,11 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
     return grads[0], grads[1], grad_state_in
 
 
+def _step_dims(x, states):
+    shape = x.shape
+    return _ints(shape[0], shape[1] if len(shape) == 3 else 1, shape[-1], states)
+
+
 def gated_recurrence_step(x, gate, state, form: str = "sigmoid", slots=None, out=None):
     """One token of gated_recurrence per row, the states updated in place. Returns h.
 
@@ -281,9 +294,10 @@ def gated_recurrence_step(x, gate, state, form: str = "sigmoid", slots=None, out
     _f32(state, "state", (P, *shape[1:]), dev)
     if slots is not None:
         _require(slots, "slots", shape[:1], torch.int32, dev)
+    B, H, d, P = _step_dims(x, P)
     out = _output(out, "out", x)
-    _call("retention_gated_recurrence_step", x, _view(x), _view(gate), _view(out), shape[0],
-          shape[1] if len(shape) == 3 else 1, shape[-1], code, dt, state.data_ptr(), P, _ptr(slots))
+    _call("retention_gated_recurrence_step", x, _view(x), _view(gate), _view(out), B, H, d, code, dt,
+          state.data_ptr(), P, _ptr(slots))
     return out
 
 
@@ -304,7 +318,7 @@ def _norm_struct(norm, n, device):
 
 
 def _head_dims(t):
-    return t.size(0), t.size(1), t.size(2) if t.dim() == 4 else 1, t.size(-1)
+    return _ints(t.size(0), t.size(1), t.size(2) if t.dim() == 4 else 1, t.size(-1))
 
 
 def gated_norm(o, gate=None, norm: NormLike = GroupNorm(), out=None):
@@ -368,8 +382,8 @@ def _rows_view(t):
 
 def _row_dims(t):
     if t.dim() == 3:
-        return t.size(0), t.size(1), t.size(2)
-    return 1, math.prod(t.shape[:-1]), t.size(-1)
+        return _ints(*t.shape)
+    return _ints(1, math.prod(t.shape[:-1]), t.size(-1))
 
 
 def _rows(t, name):
@@ -398,7 +412,8 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
     dtype or float32, y has x's. ``scale`` (fp32 [D], default 1) weighs the
     branch per channel.
     """
-    dt, dev, D = _rows(x, "x"), x.device, x.size(-1)
+    dt, dev, dims = _rows(x, "x"), x.device, _row_dims(x)
+    D = dims[-1]
     stream = _stream_dtype(residual, "residual", x.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
@@ -409,7 +424,7 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
         for name, t in (("residual", residual), ("out", out), ("residual_out", residual_out)):
             _rows_layout(t, name)
     _call("retention_residual_norm", x, _rows_view(x), _rows_view(residual), _rows_view(out), _rows_view(residual_out),
-          *_row_dims(x), dt, _CODES[stream], n, _ptr(scale), float(alpha))
+          *dims, dt, _CODES[stream], n, _ptr(scale), float(alpha))
     return out, residual_out
 
 
@@ -432,7 +447,8 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     and grad_x is grad_residual, the same tensor. ``grads``: optional
     preallocated (grad_x, grad_residual), two tensors.
     """
-    dt, dev, D = _rows(grad_y, "grad_y"), grad_y.device, grad_y.size(-1)
+    dt, dev, dims = _rows(grad_y, "grad_y"), grad_y.device, _row_dims(grad_y)
+    D = dims[-1]
     if residual is not None and x is None:
         raise ValueError("residual needs x")
     row, name = (r, "r") if residual is None else (residual, "residual")
@@ -459,7 +475,6 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     dw = None if norm.weight is None else torch.empty_like(norm.weight)
     db = None if norm.bias is None else torch.empty_like(norm.bias)
     params = any(t is not None for t in (d_scale, dw, db))
-    dims = _row_dims(grad_y)
     nbytes = _lib.load().retention_residual_norm_backward_workspace_bytes(*dims, dt, params) if params else 0
     workspace, have = _workspace(workspace, nbytes, dev)
     _call("retention_residual_norm_backward", grad_y, _rows_view(grad_y), _rows_view(grad_r),

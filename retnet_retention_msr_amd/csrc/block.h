@@ -76,6 +76,7 @@ inline uint32_t scan_round(uint32_t n) {
 }
 inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, int dtype, bool backward, int form) {
   ScanPlan p{};
+  p.waves = 1;
   p.vec = dtype == 0 ? 4 : 8;
   if (d < p.vec) p.vec = 1;
   const int64_t columns = static_cast<int64_t>(H) * ((d + kScanChannels - 1) / kScanChannels);

@@ -16,7 +16,8 @@ using ret::View;
 constexpr int64_t kMaxSpan = int64_t{1} << 46;  // elements a view may span
 constexpr int kMaxChannels = 1 << 20;           // d of the recurrence
 constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // elements; offsets within a wave's tokens are 32-bit
-constexpr int64_t kMaxBlocks = int64_t{1} << 30;
+constexpr int64_t kMaxThreads = int64_t{1} << 32;  // below which a launch's stay
+constexpr int64_t kMaxStepChannels = int64_t{1} << 30;
 constexpr int kMaxSequences = 1 << 20;
 
 int status_of(hipError_t e) { return e == hipSuccess ? RET_OK : RET_ERR_HIP; }
@@ -141,7 +142,7 @@ ret::ScanPlan plan_any(int sequences, int H, int N, int max_len, bool packed, in
   ret::ScanPlan most{};
   for (int i = 0; i < 4; ++i) {
     const ret::ScanPlan p = ret::plan_scan(sequences, H, N, max_len, packed, d, dtype, i & 1, i >> 1);
-    if (p.blocks > kMaxBlocks) return ret::ScanPlan{};
+    if (p.blocks >= kMaxThreads / 64 / p.waves) return ret::ScanPlan{};
     most.blocks = most.blocks > p.blocks ? most.blocks : p.blocks;
     most.bytes = most.bytes > p.bytes ? most.bytes : p.bytes;
   }
@@ -265,7 +266,7 @@ int retention_gated_recurrence_step(const retention_view_t* x, const retention_v
   if (st != RET_OK) return st;
   if (form != RET_GATE_SIGMOID && form != RET_GATE_LOG) return RET_ERR_INVALID_ARG;
   if (!states || nstates <= 0 || (!slots && nstates < B) || misaligned(slots, 4)) return RET_ERR_INVALID_ARG;
-  if (d > kMaxChannels || static_cast<int64_t>(H) * d > kMaxBlocks) return RET_ERR_UNSUPPORTED;
+  if (d > kMaxChannels || static_cast<int64_t>(H) * d > kMaxStepChannels) return RET_ERR_UNSUPPORTED;
   Ranges ranges;
   View vx, vg, vh;
   Range r;
@@ -378,7 +379,7 @@ int retention_residual_norm(const retention_view_t* x, const retention_view_t* r
 
 size_t retention_residual_norm_backward_workspace_bytes(int B, int N, int D, int dtype, int with_params) {
   if (check_dims(B, 1, N, D, dtype) != RET_OK || D > RETENTION_MAX_MODEL_DIM || !with_params) return 0;
-  return ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::kResidualBackGroups);
+  return ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::residual_back_groups(D));
 }
 
 int retention_residual_norm_backward(const retention_view_t* grad_y, const retention_view_t* grad_r,
@@ -419,7 +420,7 @@ int retention_residual_norm_backward(const retention_view_t* grad_y, const reten
     ranges.output(g);
   }
   if (grad_scale || grad_weight || grad_bias) {
-    const size_t need = ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::kResidualBackGroups);
+    const size_t need = ret::param_bytes(1, B * N, D, ret::kResidualNormSums, ret::residual_back_groups(D));
     if (!workspace || workspace_bytes < need || misaligned(workspace, 4)) return RET_ERR_INVALID_ARG;
     ranges.output(range_of(workspace, static_cast<int64_t>(need)));
   }

@@ -349,3 +349,31 @@ def test_rows_of_many_dimensions_are_told_by_their_length():
     t = torch.zeros(2, 3, 1, 4, 16).transpose(2, 3)  # [2, 3, 4, 1, 16], 64 the stride of the 1
     assert t.is_contiguous() and t.stride(-2) == 64
     assert block._rows_view(block._rows_layout(t, "x")).stride_n == 16 and block._row_dims(t) == (1, 24, 16)
+
+
+def test_sizes_beyond_an_int_are_refused(no_library):
+    """A broadcast tensor has as many elements as it likes; its sizes reach the C library as ints."""
+    long = torch.zeros(1, 1, 8).expand(1, (1 << 32) + 3, 8)
+    for call in (lambda: block._sequences(long, None, None), lambda: block._row_dims(long),
+                 lambda: block._head_dims(long.unsqueeze(1)), lambda: block._row_dims(long.expand(1 << 20, -1, -1)),
+                 lambda: block._step_dims(long[0], 5), lambda: block._step_dims(torch.zeros(1, 8), 1 << 32),
+                 lambda: block._row_dims(torch.zeros(1, 1, 1, 8).expand(1 << 20, 1 << 10, 1 << 10, 8))):
+        with pytest.raises(ValueError, match="too large"):
+            call()
+    x, cu = torch.zeros(1, 8, 16), torch.tensor([0, 3, 8], dtype=torch.int32)
+    assert block._sequences(x, cu, (1 << 32) + 5)[3] == 8  # no sequence is longer than the row
+
+
+def test_launches_beyond_the_grid_are_refused(lib):
+    """A launch holds at most 2^32 threads: 2^26 units of one wave each are too many, one XCD's round less is not."""
+    for B, want in ((1 << 26, UNSUPPORTED), ((1 << 26) - 8, 0)):
+        if want or SHIM:
+            assert recurrence(lib, B=B, H=1, N=1, h=A[11] + (1 << 40), strides=(0, 0, 0), h_strides=(64, 0, 0)) == want
+
+
+def test_residual_norm_backward_workspace_is_what_its_launch_fills(lib):
+    """Three sums of D values for each of 1024 workgroups, 512 for rows beyond 2048 values."""
+    f = lib.retention_residual_norm_backward_workspace_bytes
+    assert f(1, 1 << 20, 2048, 1, 1) == 1024 * 3 * 2048 * 4
+    assert f(1, 1 << 20, 4096, 1, 1) == 512 * 3 * 4096 * 4
+    assert f(1, 100, 4096, 1, 1) == 100 * 3 * 4096 * 4 and f(1, 100, 4096, 1, 0) == 0
