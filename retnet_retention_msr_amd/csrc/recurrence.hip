@@ -40,6 +40,8 @@ namespace ret {
 
 namespace {
 
+constexpr int64_t kScanCacheBytes = int64_t{200} << 20;  // of the 256 MiB Infinity Cache
+
 struct Piece {
   int64_t first;  // its first token in the row
   int len;
@@ -379,8 +381,8 @@ __device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const 
 // 5.1), 4 x 8192 x 4096 150 us. With few units a tile waits for the slowest of
 // those before it: 65536 x 2048 (32 units) 174 us (4.6 TB/s), 32768 x 256 (4)
 // 22 us (2.3 TB/s). Rows that are no multiple of a cache line move up to a
-// quarter more bytes than theirs: 4 x 7501 x 1001 fp32 95 us (3.8 TB/s).
-template <typename T, int FORM, int V, int E>
+// quarter more bytes than theirs: 4 x 7501 x 1001 fp32 87 us (4.1 TB/s).
+template <typename T, int FORM, int V, int E, bool CACHED>
 __global__ void __launch_bounds__(64 * kScanMaxWaves, 4)
 recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_in, float* state_out, ScanWords w,
                   uint32_t units, int tiles) {
@@ -486,14 +488,14 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
-      store_channels<false, T, V>(hb + i * out.sn + ho, y, at);
+      store_channels<CACHED, T, V>(hb + i * out.sn + ho, y, at);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
-      if (t0 + i < len) store_channels<false, T, V>(hr + (t0 + i) * out.sn + at.start, y, at);
+      if (t0 + i < len) store_channels<CACHED, T, V>(hr + (t0 + i) * out.sn + at.start, y, at);
     }
   }
 }
@@ -760,14 +762,25 @@ hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const Vie
   const hipError_t e = scan_words(p, workspace, &words, stream);
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
-#define RET_SCAN(T, FORM, V, E)                                                                           \
-  recurrence_kernel<T, FORM, V, E><<<grid, block, 0, stream>>>(x, gate, h, q, state_in, state_out, words, \
-                                                               static_cast<uint32_t>(p.units),            \
-                                                               static_cast<int>(p.tiles))
-#define RET_SCAN_VEC(T, FORM, V)                            \
-  do {                                                      \
-    if (p.vec == V) RET_SCAN(T, FORM, V, kScanRows);        \
-    else RET_SCAN(T, FORM, 1, kScanNarrowRows);             \
+  // Rows that do not all begin on a cache line: the pieces that two workgroups
+  // write meet within lines and go through the caches (8 x 4096 x 4104 bf16 183
+  // us against 243 past them, 64 x 1024 x 1032 100 against 130, 64 x 640 x 1001
+  // fp32 108 against 125). Where x, gate and h are small enough for the inputs
+  // to be in the Infinity Cache still, results past it leave them there (176 MB,
+  // 10749 x 2728 bf16: 54 against 46; 240 MB, 2 x 20000 x 1001 bf16: 74 and 75).
+  const int64_t size = dtype == 0 ? 4 : 2;
+  const int64_t rows = int64_t{q.cu ? 1 : q.S} * q.H * q.N;
+  const bool cached = h.sn * size % 128 != 0 && 3 * rows * q.d * size > kScanCacheBytes;
+#define RET_SCAN(T, FORM, V, E, CACHED)                                                                \
+  recurrence_kernel<T, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(x, gate, h, q, state_in,        \
+                                                                       state_out, words,               \
+                                                                       static_cast<uint32_t>(p.units), \
+                                                                       static_cast<int>(p.tiles))
+#define RET_SCAN_VEC(T, FORM, V)                                     \
+  do {                                                               \
+    if (p.vec == V && cached) RET_SCAN(T, FORM, V, kScanRows, true); \
+    else if (p.vec == V) RET_SCAN(T, FORM, V, kScanRows, false);     \
+    else RET_SCAN(T, FORM, 1, kScanNarrowRows, true);                \
   } while (0)
   if (dtype == 0) {
     if (form == 0) RET_SCAN_VEC(float, 0, 4);
@@ -794,8 +807,7 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
   // write meet within lines, and two results of them fare better through the
   // caches (bf16: 4 x 7501 x 1001 111 us against 131, 55 x 193 x 3824 108
   // against 132, 10749 x 2728 105 against 108; fp32: 4 x 7501 x 1001 190
-  // against 203, 4 x 19454 x 696 321 against 313). The forward's one result
-  // mostly does not: 55 against 50 and 53 against 47 at the first and third.
+  // against 203, 4 x 19454 x 696 321 against 313).
   const int64_t size = dtype == 0 ? 4 : 2;
   const bool cached = grad_x.sn * size % 128 != 0 || grad_gate.sn * size % 128 != 0;
 #define RET_SCAN(T, FORM, V, E, CACHED)                                                                    \
