@@ -92,6 +92,35 @@ def _same(t, name, like, dtype=None):
     return _last_contiguous(t, name)
 
 
+class _Like:
+    """What the tensors of a call share with the first of them: its shape, dtype and device, asked for once. ``flat``:
+    taken as rows of a contiguous tensor."""
+
+    __slots__ = ("t", "shape", "dtype", "device", "flat")
+
+    def __init__(self, t, flat=False):
+        self.t, self.shape, self.dtype, self.device, self.flat = t, t.shape, t.dtype, t.device, flat
+
+    def view(self, t, name, dtype=None):
+        """The retention_view_t of ``t``, after the checks of _same()."""
+        dtype = dtype or self.dtype
+        if (self.flat or not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != self.shape
+                or t.device != self.device):
+            return (_flat_view(_same(t, name, self.t, dtype), name) if self.flat else
+                    _view(_same(t, name, self.t, dtype)))
+        s = t.stride()
+        if s[-1] != 1:
+            _last_contiguous(t, name)
+        return _lib.View(t.data_ptr(), s[0], s[1], s[-2])
+
+    def output(self, t, name, dtype=None):
+        """(tensor, view) of an output, allocated if None."""
+        if t is not None:
+            return t, self.view(t, name, dtype)
+        t = _new(self.t, dtype)
+        return t, (_flat_view(t, name) if self.flat else _view(t))
+
+
 def _f32(t, name, shape, device):
     """``t`` is a contiguous float32 tensor of this shape on ``device``."""
     if (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == shape and t.device == device
@@ -108,11 +137,11 @@ def _ints(*sizes):
 
 
 def _new(like, dtype=None):
+    if dtype is None or dtype is like.dtype:
+        if like.is_contiguous():
+            return torch.empty_like(like)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
-
-
-def _output(t, name, like, dtype=None):
-    return _new(like, dtype) if t is None else _same(t, name, like, dtype)
 
 
 def _ptr(t):
@@ -216,17 +245,17 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     an output allocated here they are undefined.
     """
     dt = _activations(x, "x", (3, 4))
-    _same(gate, "gate", x)
-    code = _form(form)
+    like = _Like(x)
+    gate_view, code = like.view(gate, "gate"), _form(form)
     dims, states, S, max_len = _sequences(x, cu_seqlens, max_len)
-    dev = x.device
-    out = _output(out, "out", x)
+    dev = like.device
+    out, out_view = like.output(out, "out")
     if state_in is not None:
         _f32(state_in, "state_in", states, dev)
     state_out = _state_to_fill(state_out, "state_out", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence", x, _view(x), _view(gate), _view(out), *dims, code, dt, _ptr(state_in),
+    _call("retention_gated_recurrence", x, _view(x), gate_view, out_view, *dims, code, dt, _ptr(state_in),
           _ptr(state_out), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have)
     return out, state_out
 
@@ -245,34 +274,30 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
     """
     code = _form(form)
     dt = _activations(gate, "gate", (3, 4))
-    _same(grad_h, "grad_h", gate)
-    _same(h, "h", gate)
-    if x is not None:
-        _same(x, "x", gate)
-    elif code == 0:
+    like = _Like(gate)
+    if x is None and code == 0:
         raise ValueError("the sigmoid form needs x")
+    inputs = (like.view(grad_h, "grad_h"), None if x is None else like.view(x, "x"), _view(gate), like.view(h, "h"))
     dims, states, S, max_len = _sequences(gate, cu_seqlens, max_len)
-    dev = gate.device
+    dev = like.device
     if grads is None:
-        grads = (_new(gate), _new(gate))
-    if len(grads) != 2:
+        grads = None, None
+    elif len(grads) != 2 or any(t is None for t in grads):
         raise ValueError("grads must be (grad_x, grad_gate)")
-    for name, t in zip(("grad_x", "grad_gate"), grads):
-        _same(t, name, gate)
+    (grad_x, dx_view), (grad_gate, dg_view) = like.output(grads[0], "grad_x"), like.output(grads[1], "grad_gate")
     for name, t in (("state_in", state_in), ("grad_state_out", grad_state_out)):
         if t is not None:
             _f32(t, name, states, dev)
     grad_state_in = _state_to_fill(grad_state_in, "grad_state_in", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence_backward", gate, _view(grad_h), _view(x), _view(gate), _view(h),
-          _view(grads[0]), _view(grads[1]), *dims, code, dt, _ptr(state_in), _ptr(grad_state_out),
-          _ptr(grad_state_in), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have)
-    return grads[0], grads[1], grad_state_in
+    _call("retention_gated_recurrence_backward", gate, *inputs, dx_view, dg_view, *dims, code, dt,
+          _ptr(state_in), _ptr(grad_state_out), _ptr(grad_state_in), _ptr(cu_seqlens), S, max_len, _ptr(workspace),
+          have)
+    return grad_x, grad_gate, grad_state_in
 
 
-def _step_dims(x, states):
-    shape = x.shape
+def _step_dims(shape, states):
     return _ints(shape[0], shape[1] if len(shape) == 3 else 1, shape[-1], states)
 
 
@@ -286,23 +311,25 @@ def gated_recurrence_step(x, gate, state, form: str = "sigmoid", slots=None, out
     another in row order.
     """
     dt = _activations(x, "x", (2, 3))
-    _same(gate, "gate", x)
-    code, dev, shape = _form(form), x.device, x.shape
+    like = _Like(x)
+    gate_view, code, dev, shape = like.view(gate, "gate"), _form(form), like.device, like.shape
     if not isinstance(state, torch.Tensor) or state.dim() != len(shape):
         raise ValueError(f"state must be a tensor with {len(shape)} dimensions")
     P = shape[0] if slots is None else state.size(0)
     _f32(state, "state", (P, *shape[1:]), dev)
     if slots is not None:
         _require(slots, "slots", shape[:1], torch.int32, dev)
-    B, H, d, P = _step_dims(x, P)
-    out = _output(out, "out", x)
-    _call("retention_gated_recurrence_step", x, _view(x), _view(gate), _view(out), B, H, d, code, dt,
+    B, H, d, P = _step_dims(shape, P)
+    out, out_view = like.output(out, "out")
+    _call("retention_gated_recurrence_step", x, _view(x), gate_view, out_view, B, H, d, code, dt,
           state.data_ptr(), P, _ptr(slots))
     return out
 
 
 # ---------------------------------------------------------------------------
 # Norms
+
+_ROWS = range(1, 65)  # dimensions of a tensor of rows
 
 
 def _norm_struct(norm, n, device):
@@ -317,8 +344,8 @@ def _norm_struct(norm, n, device):
     return _lib.NormStruct(norm.eps, getattr(norm, "rms", False), weight, bias)
 
 
-def _head_dims(t):
-    return _ints(t.size(0), t.size(1), t.size(2) if t.dim() == 4 else 1, t.size(-1))
+def _head_dims(shape):
+    return _ints(shape[0], shape[1], shape[2] if len(shape) == 4 else 1, shape[-1])
 
 
 def gated_norm(o, gate=None, norm: NormLike = GroupNorm(), out=None):
@@ -331,12 +358,12 @@ def gated_norm(o, gate=None, norm: NormLike = GroupNorm(), out=None):
     as an operator of its own, for training, where the backward needs o.
     """
     dt = _activations(o, "o", (3, 4))
-    if gate is not None:
-        _same(gate, "gate", o)
-    dims = _head_dims(o)
-    n = _norm_struct(norm, dims[1] * dims[3], o.device)
-    out = _output(out, "out", o)
-    _call("retention_gated_norm", o, _view(o), _view(gate), _view(out), *dims, dt, n)
+    like = _Like(o)
+    gate_view = None if gate is None else like.view(gate, "gate")
+    dims = _head_dims(like.shape)
+    n = _norm_struct(norm, dims[1] * dims[3], like.device)
+    out, out_view = like.output(out, "out")
+    _call("retention_gated_norm", o, _view(o), gate_view, out_view, *dims, dt, n)
     return out
 
 
@@ -350,52 +377,43 @@ def gated_norm_backward(grad_y, o, gate=None, norm: NormLike = GroupNorm(), grad
     None without a gate, grad_weight and grad_bias (fp32 [H*d]) where the norm has no weight or bias. ``grads``:
     optional preallocated (grad_o, grad_gate). grad_o is what chunkwise_backward takes as grad_o."""
     dt = _activations(o, "o", (3, 4))
-    _same(grad_y, "grad_y", o)
-    if gate is not None:
-        _same(gate, "gate", o)
-    dims, dev = _head_dims(o), o.device
+    like = _Like(o)
+    inputs = like.view(grad_y, "grad_y"), _view(o), None if gate is None else like.view(gate, "gate")
+    dims, dev = _head_dims(like.shape), like.device
     n = _norm_struct(norm, dims[1] * dims[3], dev)
     if grads is None:
-        grads = (_new(o), None if gate is None else _new(o))
-    if len(grads) != 2 or (grads[1] is None) != (gate is None):
+        grads = None, None
+    elif len(grads) != 2 or grads[0] is None or (grads[1] is None) != (gate is None):
         raise ValueError("grads must be (grad_o, grad_gate), grad_gate None without a gate")
-    _same(grads[0], "grad_o", o)
-    if gate is not None:
-        _same(grads[1], "grad_gate", o)
+    grad_o, do_view = like.output(grads[0], "grad_o")
+    grad_gate, dg_view = (None, None) if gate is None else like.output(grads[1], "grad_gate")
     dw = None if norm.weight is None else torch.empty_like(norm.weight)
     db = None if norm.bias is None else torch.empty_like(norm.bias)
     params = dw is not None or db is not None
     nbytes = _lib.load().retention_gated_norm_backward_workspace_bytes(*dims, dt, params) if params else 0
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_norm_backward", o, _view(grad_y), _view(o), _view(gate), _view(grads[0]), _view(grads[1]),
-          *dims, dt, n, _ptr(dw), _ptr(db), _ptr(workspace), have)
-    return grads[0], grads[1], dw, db
+    _call("retention_gated_norm_backward", o, *inputs, do_view, dg_view, *dims, dt, n, _ptr(dw), _ptr(db),
+          _ptr(workspace), have)
+    return grad_o, grad_gate, dw, db
 
 
-def _rows_view(t):
-    """Rows of the last dimension: [B, N, D] or [R, D] with any strides, one, or those of a contiguous tensor of more
-    dimensions, which lie D apart (the stride of a dimension of one element says nothing)."""
-    if t is None or 2 <= t.dim() <= 3:
-        return _view(t)
+def _rows_like(t):
+    """_Like() of rows of the last dimension: [B, N, D] or [R, D] with any strides, one row, or those of a contiguous
+    tensor of more dimensions."""
+    return _Like(t, not 2 <= t.dim() <= 3)
+
+
+def _flat_view(t, name):
+    """The rows of a contiguous tensor, which lie D apart (the stride of a dimension of one element says nothing)."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous when it has more than three dimensions")
     return _lib.View(t.data_ptr(), 0, 0, t.size(-1))
 
 
-def _row_dims(t):
-    if t.dim() == 3:
-        return _ints(*t.shape)
-    return _ints(1, math.prod(t.shape[:-1]), t.size(-1))
-
-
-def _rows(t, name):
-    dt = _activations(t, name, range(1, 65))
-    _rows_layout(t, name)
-    return dt
-
-
-def _rows_layout(t, name):
-    if t.dim() > 3 and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous when it has more than three dimensions")
-    return t
+def _row_dims(shape):
+    if len(shape) == 3:
+        return _ints(*shape)
+    return _ints(1, math.prod(shape[:-1]), shape[-1])
 
 
 def _stream_dtype(t, name, dtype):
@@ -412,19 +430,18 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
     dtype or float32, y has x's. ``scale`` (fp32 [D], default 1) weighs the
     branch per channel.
     """
-    dt, dev, dims = _rows(x, "x"), x.device, _row_dims(x)
+    dt, like = _activations(x, "x", _ROWS), _rows_like(x)
+    dims, dev = _row_dims(like.shape), like.device
     D = dims[-1]
-    stream = _stream_dtype(residual, "residual", x.dtype)
+    stream = _stream_dtype(residual, "residual", like.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
         _f32(scale, "scale", (D,), dev)
-    out, residual_out = _output(out, "out", x), _output(residual_out, "residual_out", x, stream)
-    _same(residual, "residual", x, stream)
-    if x.dim() > 3:
-        for name, t in (("residual", residual), ("out", out), ("residual_out", residual_out)):
-            _rows_layout(t, name)
-    _call("retention_residual_norm", x, _rows_view(x), _rows_view(residual), _rows_view(out), _rows_view(residual_out),
-          *dims, dt, _CODES[stream], n, _ptr(scale), float(alpha))
+    inputs = like.view(x, "x"), like.view(residual, "residual", stream)
+    out, out_view = like.output(out, "out")
+    residual_out, r_view = like.output(residual_out, "residual_out", stream)
+    _call("retention_residual_norm", x, *inputs, out_view, r_view, *dims, dt, _CODES[stream], n, _ptr(scale),
+          float(alpha))
     return out, residual_out
 
 
@@ -447,39 +464,33 @@ def residual_norm_backward(grad_y, r, norm: NormLike, grad_r=None, x=None, scale
     and grad_x is grad_residual, the same tensor. ``grads``: optional
     preallocated (grad_x, grad_residual), two tensors.
     """
-    dt, dev, dims = _rows(grad_y, "grad_y"), grad_y.device, _row_dims(grad_y)
+    dt, like = _activations(grad_y, "grad_y", _ROWS), _rows_like(grad_y)
+    dims, dev = _row_dims(like.shape), like.device
     D = dims[-1]
     if residual is not None and x is None:
         raise ValueError("residual needs x")
     row, name = (r, "r") if residual is None else (residual, "residual")
-    stream = _stream_dtype(row, name, grad_y.dtype)
+    stream = _stream_dtype(row, name, like.dtype)
     n = _norm_struct(norm, D, dev)
     if scale is not None:
         _f32(scale, "scale", (D,), dev)
+    shared = grads is None and scale is None and float(alpha) == 1.0 and stream == like.dtype
     if grads is None:
-        d_res = _new(grad_y, stream)
-        shared = scale is None and float(alpha) == 1.0 and stream == grad_y.dtype
-        grads = (d_res if shared else _new(grad_y), d_res)
-    else:
-        shared = False
-        if len(grads) != 2:
-            raise ValueError("grads must be (grad_x, grad_residual)")
-    _same(grads[0], "grad_x", grad_y)
-    for what, t in ((name, row), ("grad_r", grad_r), ("grad_residual", grads[1])):
-        if t is not None:
-            _rows_layout(_same(t, what, grad_y, stream), what)
-    if x is not None:
-        _rows_layout(_same(x, "x", grad_y), "x")
-    _rows_layout(grads[0], "grad_x")
+        grads = None, None
+    elif len(grads) != 2 or any(t is None for t in grads):
+        raise ValueError("grads must be (grad_x, grad_residual)")
+    grad_residual, d_res_view = like.output(grads[1], "grad_residual", stream)
+    grad_x, dx_view = (grad_residual, None) if shared else like.output(grads[0], "grad_x")
+    row_view, x_view = like.view(row, name, stream), None if x is None else like.view(x, "x")
+    views = (like.view(grad_y, "grad_y"), None if grad_r is None else like.view(grad_r, "grad_r", stream),
+             row_view if residual is None else None, x_view if scale is not None or residual is not None else None,
+             None if residual is None else row_view, dx_view, d_res_view)
     d_scale = torch.empty_like(scale) if scale is not None and x is not None else None
     dw = None if norm.weight is None else torch.empty_like(norm.weight)
     db = None if norm.bias is None else torch.empty_like(norm.bias)
     params = any(t is not None for t in (d_scale, dw, db))
     nbytes = _lib.load().retention_residual_norm_backward_workspace_bytes(*dims, dt, params) if params else 0
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_residual_norm_backward", grad_y, _rows_view(grad_y), _rows_view(grad_r),
-          None if residual is not None else _rows_view(r),
-          _rows_view(x if d_scale is not None or residual is not None else None), _rows_view(residual),
-          None if shared else _rows_view(grads[0]), _rows_view(grads[1]), *dims, dt,
-          _CODES[stream], n, _ptr(scale), float(alpha), _ptr(d_scale), _ptr(dw), _ptr(db), _ptr(workspace), have)
-    return grads[0], grads[1], d_scale, dw, db
+    _call("retention_residual_norm_backward", grad_y, *views, *dims, dt, _CODES[stream], n, _ptr(scale), float(alpha),
+          _ptr(d_scale), _ptr(dw), _ptr(db), _ptr(workspace), have)
+    return grad_x, grad_residual, d_scale, dw, db

@@ -278,6 +278,12 @@ def test_host_tensors_and_non_tensors_are_refused(no_library):
 def test_same_checks_device_dtype_shape_and_layout(bad, match):
     with pytest.raises(ValueError, match=match):
         block._same(bad, "gate", torch.zeros(2, 8, 16))
+    with pytest.raises(ValueError, match=match):
+        block._Like(torch.zeros(2, 8, 16)).view(bad, "gate")
+
+
+def _rows_view(t):
+    return block._rows_like(t).view(t, "x")
 
 
 def test_strided_views_are_taken_as_they_are():
@@ -291,11 +297,11 @@ def test_strided_views_are_taken_as_they_are():
     assert (v.stride_b, v.stride_h) == (8 * 48, 16)
     v = block._view(wide[:, 0])  # [B, D]
     assert v.stride_b == 320
-    v = block._rows_view(torch.zeros(2, 3, 4, 16))
-    assert v.stride_n == 16 and block._row_dims(torch.zeros(2, 3, 4, 16)) == (1, 24, 16)
-    v = block._rows_view(wide[0])  # [R, D]
-    assert v.stride_n == 40 and block._row_dims(wide[0]) == (1, 8, 40)
-    assert block._row_dims(torch.zeros(16)) == (1, 1, 16)
+    v = _rows_view(torch.zeros(2, 3, 4, 16))
+    assert v.stride_n == 16 and block._row_dims((2, 3, 4, 16)) == (1, 24, 16)
+    v = _rows_view(wide[0])  # [R, D]
+    assert v.stride_n == 40 and block._row_dims(wide[0].shape) == (1, 8, 40)
+    assert block._row_dims((16,)) == (1, 1, 16)
 
 
 def test_unsupported_dtypes_are_type_errors():
@@ -348,16 +354,17 @@ def test_rows_of_many_dimensions_are_told_by_their_length():
     """Contiguous is said whatever the stride of a dimension of one element: the rows of such a tensor are D apart."""
     t = torch.zeros(2, 3, 1, 4, 16).transpose(2, 3)  # [2, 3, 4, 1, 16], 64 the stride of the 1
     assert t.is_contiguous() and t.stride(-2) == 64
-    assert block._rows_view(block._rows_layout(t, "x")).stride_n == 16 and block._row_dims(t) == (1, 24, 16)
+    assert _rows_view(t).stride_n == 16 and block._row_dims(t.shape) == (1, 24, 16)
+    with pytest.raises(ValueError, match="contiguous when"):
+        _rows_view(torch.zeros(2, 3, 4, 32)[..., :16])
 
 
 def test_sizes_beyond_an_int_are_refused(no_library):
     """A broadcast tensor has as many elements as it likes; its sizes reach the C library as ints."""
     long = torch.zeros(1, 1, 8).expand(1, (1 << 32) + 3, 8)
-    for call in (lambda: block._sequences(long, None, None), lambda: block._row_dims(long),
-                 lambda: block._head_dims(long.unsqueeze(1)), lambda: block._row_dims(long.expand(1 << 20, -1, -1)),
-                 lambda: block._step_dims(long[0], 5), lambda: block._step_dims(torch.zeros(1, 8), 1 << 32),
-                 lambda: block._row_dims(torch.zeros(1, 1, 1, 8).expand(1 << 20, 1 << 10, 1 << 10, 8))):
+    for call in (lambda: block._sequences(long, None, None), lambda: block._row_dims(long.shape),
+                 lambda: block._head_dims(long.unsqueeze(1).shape), lambda: block._step_dims((1, 8), 1 << 32),
+                 lambda: block._step_dims(long[0].shape, 5), lambda: block._row_dims((1 << 20, 1 << 10, 1 << 10, 8))):
         with pytest.raises(ValueError, match="too large"):
             call()
     x, cu = torch.zeros(1, 8, 16), torch.tensor([0, 3, 8], dtype=torch.int32)
