@@ -724,6 +724,26 @@ def test_outputs_past_two_to_the_31_elements():
     assert torch.equal(y[-k:], y2)
 
 
+@pytest.mark.parametrize("shape, pitch, form, dtype", [
+    ((1, 17600, 1001), 1001, "sigmoid", F32), ((3, 12000, 1003), 1010, "log", BF16), ((300, 130, 1000), 1004, "sigmoid", BF16)])
+def test_wide_results_in_rows_that_begin_anywhere(shape, pitch, form, dtype):
+    """Results too large to leave the inputs in the caches, in rows that do not begin on cache lines: some channels
+    (the recurrence is per channel) of a few rows against the oracle, and nothing written beside the rows."""
+    _announce(f"wide results {shape} pitch {pitch} {form} {dtype}")
+    B, N, D = shape
+    at = [*range(10), *range(60, 70), *range(D - 70, D - 60), *range(D - 9, D)]
+    x, g = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form)
+    s0 = _randn((B, D), 3)
+    wide = torch.full((B, N, pitch), float("nan"), dtype=dtype, device=DEV)
+    h, s1 = ret.gated_recurrence(x.to(DEV), g.to(DEV), form, state_in=s0.to(DEV), state_out=True, out=wide[..., :D])
+    rows = [0, B - 1]
+    args = (x[rows][..., at], g[rows][..., at], form, s0[rows][..., at])
+    (ref, end), (e, e_end) = orc.recurrence(*args), orc.recurrence_error(*args)
+    _check(h[rows][..., at], ref, e, "h")
+    _check(s1[rows][..., at], end, e_end, "state")
+    assert bool(torch.isnan(wide[..., D:]).all()) and not bool(torch.isnan(h).any())
+
+
 def test_large_offsets():
     """Rows whose element offsets pass 2^31: the last rows of a tall strided tensor, checked on their own."""
     _announce("offsets past 2^31")
