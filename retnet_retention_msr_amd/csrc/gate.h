@@ -8,12 +8,14 @@ namespace ret {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // sigmoid(g) and 1 - sigmoid(g), each to a few units in the last place of its
-// own size: with e = exp(-g), a = 1 / (1 + e) and 1 - a = e a. At g = -inf the
-// product is inf * 0 and the minimum takes the 1.
+// own size: with e = exp(-g), a = 1 / (1 + e), and 1 - a = e a where a is the
+// larger of the two, else by subtraction (e overflows there, or its
+// reciprocal is less than the least normal number, which the hardware's makes
+// 0). A NaN stays one in both.
 __device__ __forceinline__ void sigmoid_pair(float g, float& a, float& one_less) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * g);
   a = __builtin_amdgcn_rcpf(1.0f + e);
-  one_less = __builtin_fminf(e * a, 1.0f);
+  one_less = g < 0.0f ? 1.0f - a : e * a;
 }
 
 // Workgroup barrier that orders LDS accesses only: outstanding global loads

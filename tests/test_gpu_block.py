@@ -233,6 +233,42 @@ def test_offsets_out_of_range_are_clamped():
     assert torch.equal(h, h2) and torch.equal(s, s2)
 
 
+def test_gates_of_every_size():
+    """Gates from -95 to 95, through those whose e^-g or whose decay leaves fp32's normal numbers (a product with such a
+    decay may be 0: off by less than 2^-126 times its other factors, here below 8), in the recurrence, its backward, its
+    step and the norm's gate."""
+    _announce("gates of every size")
+    g = torch.linspace(-95, 95, 1901).view(1, 1, -1)
+    x, dh, s0 = _randn(g.shape, 1), _randn(g.shape, 2), _randn((1, 1901), 3)
+    dev = [t.to(DEV) for t in (x, g, dh, s0)]
+    tiny = 2.0 ** -123
+    for form, gate in (("sigmoid", g), ("log", -g.abs())):
+        gd = gate.to(DEV)
+        h, s1 = ret.gated_recurrence(dev[0], gd, form, state_in=dev[3], state_out=True)
+        (ref, _), (e, _) = orc.recurrence(x, gate, form, s0), orc.recurrence_error(x, gate, form, s0)
+        _check(h, ref, e + tiny, "h")
+        state = dev[3].clone()
+        step = ret.gated_recurrence_step(dev[0][0], gd[0], state, form)
+        _check(step[None], ref, e + tiny, "step")
+        assert torch.equal(state, step) and torch.equal(s1, h[:, 0])
+        got = ret.gated_recurrence_backward(dev[2], dev[0], gd, h, form, state_in=dev[3], grad_state_in=True)
+        refs = orc.recurrence_backward(dh, x, gate, h.cpu(), form, s0, None)
+        errs = orc.recurrence_backward_error(dh, x, gate, h.cpu(), form, s0, None)
+        for t, r, e, what in zip(got, refs, errs, ("grad_x", "grad_gate", "grad_state_in")):
+            _check(t, r, e + tiny, what)
+    # The norm's gate multiplies such a decay by the gate itself (below 2^6.5) and by factors below 2^6 together.
+    tiny = 2.0 ** -113
+    shape = (1, 2, 1, 950)
+    gate, o, dy = g.reshape(-1)[:1900].view(shape), _randn(shape, 4), _randn(shape, 5)
+    norm = ret.Norm(EPS)
+    args = (o, gate, None, None, EPS, False)
+    _check(ret.gated_norm(o.to(DEV), gate.to(DEV), norm), orc.gated_norm(*args), orc.gated_norm_error(*args) + tiny, "y")
+    got = ret.gated_norm_backward(dy.to(DEV), o.to(DEV), gate.to(DEV), norm)
+    refs, errs = orc.gated_norm_backward(dy, *args), orc.gated_norm_backward_error(dy, *args)
+    for t, r, e, what in zip(got[:2], refs, errs, ("grad_o", "grad_gate")):
+        _check(t, r, e + tiny, what)
+
+
 def test_states_in_place_and_fused_gradient_buffers():
     """state_out may be state_in, grad_state_in grad_state_out, and the gradients two halves of one tensor."""
     _announce("states in place")
