@@ -146,9 +146,12 @@ inline int gated_back_groups(int heads, int rows, int at_once) {
   return turns < 512 ? 512 : turns < kGatedBackGroups ? static_cast<int>(turns) : kGatedBackGroups;
 }
 // As many workgroups as are at work at once: four of 256 threads to a CU, two
-// of 512.
+// of 512, one of 1024 (8192 x 8192 with an fp32 stream 222 us, with twice as
+// many 236: each leaves a row of partial sums).
 constexpr int kResidualBackGroups = 1024;
-inline int residual_back_groups(int d) { return d <= 2048 ? kResidualBackGroups : kResidualBackGroups / 2; }
+inline int residual_back_groups(int d) {
+  return d <= 2048 ? kResidualBackGroups : d <= 4096 ? kResidualBackGroups / 2 : kResidualBackGroups / 4;
+}
 // Bytes of the backward's partial sums: a row of `sums` times d floats for
 // each of its workgroups (whatever the rows a workgroup takes at a time).
 inline size_t param_bytes(int heads, int rows, int d, int sums, int groups) {

@@ -496,11 +496,63 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
   }
 }
 
+// A thread's running sums, in registers or, where those of a row's three
+// tensors leave no room for them, in LDS of its own (4096 x 16384, whole
+// backward: bf16 171 us against 197, fp32 367 against 525).
+template <int E, bool LDS>
+struct RunningSums {
+  float v[E];
+  __device__ __forceinline__ explicit RunningSums(float4*) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  }
+  template <typename F>
+  __device__ __forceinline__ void add(F term) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = term(e, v[e]);
+  }
+  __device__ __forceinline__ void get(float (&x)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = v[e];
+  }
+};
+template <int E>
+struct RunningSums<E, true> {
+  float4* at;  // E / 4 words of four, a workgroup's threads side by side
+  __device__ __forceinline__ explicit RunningSums(float4* all) : at(all + threadIdx.x) {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) at[k * blockDim.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  template <typename F>
+  __device__ __forceinline__ void add(F term) {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+      float4 w = at[k * blockDim.x];
+      w.x = term(4 * k, w.x);
+      w.y = term(4 * k + 1, w.y);
+      w.z = term(4 * k + 2, w.z);
+      w.w = term(4 * k + 3, w.w);
+      at[k * blockDim.x] = w;
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+      const float4 w = at[k * blockDim.x];
+      x[4 * k] = w.x;
+      x[4 * k + 1] = w.y;
+      x[4 * k + 2] = w.z;
+      x[4 * k + 3] = w.w;
+    }
+  }
+};
+
 // The row is r or, with `residual`, formed again from it and x. Bound by HBM up
 // to 8192 values a row: the case above 235 us with the parameters' sums (5.1
-// TB/s). Wider rows take 16 values a thread in 1024 threads, whose 128 registers
-// do not hold a row's three tensors and three sums: 4096 x 16384 199 us (2.7
-// TB/s).
+// TB/s), 8192 x 8192 222 us (5.4 TB/s). Wider rows take 16 values a thread in
+// 1024 threads, two of their three sums in LDS; a CU then has one row at a time
+// and the next one's loads wait for it: 4096 x 16384 bf16 159 us (3.4 TB/s),
+// fp32 343 us (4.7 TB/s).
 template <typename T, typename TR, int L, int V, int K, bool MASK>
 __global__ void __launch_bounds__(threads_of(L), (sizeof(T) == 2 && V * K <= 8) || L == 1024 ? 4 : 2)
 residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, View dx, View dres, int rows, int N,
@@ -512,11 +564,10 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, V
   const int g = threadIdx.x / L;
   const P part(threadIdx.x % L, D);
   const Held<P> scales(part, scale), weights(part, n.weight);
-  float sums[kResidualNormSums][E];
-#pragma unroll
-  for (int s = 0; s < kResidualNormSums; ++s)
-#pragma unroll
-    for (int e = 0; e < E; ++e) sums[s][e] = 0.0f;
+  constexpr bool kLds = L == 1024 && E > 8;
+  __shared__ float4 held[2][kLds ? L * E / 4 : 1];
+  RunningSums<E, kLds> sum0(held[0]), sum1(held[1]);
+  RunningSums<E, false> sum2(nullptr);
   const int step = gridDim.x * G;
   RowWalk row(blockIdx.x * G + g, step, N);
   const View& from = residual.data ? residual : r;
@@ -569,10 +620,11 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, V
 #pragma unroll
     for (int e = 0; e < E; ++e) {  // q is 0 for channels that are not the thread's own
       v[e] = (v[e] - mean) * rstd;
-      sums[1][e] = fmaf(q[e], v[e], sums[1][e]);
-      sums[2][e] += q[e];
-      q[e] = rstd * (qw[e] - s1 - v[e] * s2);
+      sum2.v[e] += q[e];
     }
+    if (!kLds || partial) sum1.add([&](int e, float s) { return fmaf(q[e], v[e], s); });
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = rstd * (qw[e] - s1 - v[e] * s2);
     if (dr.data) {
       part.values(sw_now, p);
 #pragma unroll
@@ -580,8 +632,7 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, V
     }
     if (x.data) {
       part.values(xw_now, p);  // 0 for channels that are not the thread's own
-#pragma unroll
-      for (int e = 0; e < E; ++e) sums[0][e] = live ? fmaf(q[e], p[e], sums[0][e]) : sums[0][e];
+      if (!kLds || partial) sum0.add([&](int e, float s) { return live ? fmaf(q[e], p[e], s) : s; });
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = alpha * q[e];
@@ -596,10 +647,15 @@ residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, V
     }
     if (!kEarly && base + step < rows) load(base + step + g < rows);
   }
-  if (partial)
+  if (partial) {
+    float sums[kResidualNormSums][E];
+    sum0.get(sums[0]);
+    sum1.get(sums[1]);
+    sum2.get(sums[2]);
     leave_sums<kResidualNormSums, G, P>(part, sums,
                                         partial + static_cast<int64_t>(blockIdx.x) * kResidualNormSums * D, D,
                                         wanted);
+  }
 }
 
 // ---------------------------------------------------------------------------

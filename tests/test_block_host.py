@@ -379,8 +379,9 @@ def test_launches_beyond_the_grid_are_refused(lib):
 
 
 def test_residual_norm_backward_workspace_is_what_its_launch_fills(lib):
-    """Three sums of D values for each of 1024 workgroups, 512 for rows beyond 2048 values."""
+    """Three sums of D values for each of 1024 workgroups, 512 for rows beyond 2048 values, 256 beyond 4096."""
     f = lib.retention_residual_norm_backward_workspace_bytes
     assert f(1, 1 << 20, 2048, 1, 1) == 1024 * 3 * 2048 * 4
     assert f(1, 1 << 20, 4096, 1, 1) == 512 * 3 * 4096 * 4
+    assert f(1, 1 << 16, 16384, 0, 1) == 256 * 3 * 16384 * 4
     assert f(1, 100, 4096, 1, 1) == 100 * 3 * 4096 * 4 and f(1, 100, 4096, 1, 0) == 0

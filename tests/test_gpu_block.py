@@ -558,6 +558,7 @@ ROWS = [
     ((130, 1000), BF16, F32), ((33, 1023), BF16, BF16), ((9, 1024), F32, F32), ((40, 2048), BF16, F32),
     ((7, 2049), F32, F32), ((70, 4096), BF16, BF16), ((3, 5000), BF16, F32), ((5, 8192), F32, F32), ((4, 8192), BF16, F32),
     ((3, 16384), BF16, BF16), ((2, 16384), F32, F32), ((2, 16383), BF16, F32), ((4096,), BF16, BF16),
+    ((600, 9001), BF16, F32), ((300, 16384), F32, F32), ((600, 5000), BF16, BF16),
 ]
 
 
