@@ -1,10 +1,10 @@
 // Loads and stores of V neighbouring elements of a row as floats, in one
 // access of V elements. The address need only be aligned to an element: global
 // accesses of up to 16 bytes may lie anywhere on this GPU (the compiler's
-// default for it), so rows of odd widths and offsets take the same path. store() is non-temporal
-// (long results that the kernel does not read again: 4% faster forward
-// recurrence at 4 x 8192 x 4096), keep() is not (states that the next step
-// reads).
+// default for it), so rows of odd widths and offsets take the same path.
+// store() is non-temporal (long results that the kernel does not read again: 4%
+// faster forward recurrence at 4 x 8192 x 4096), keep() is not (states that the
+// next step reads, pieces of cache lines).
 #pragma once
 
 #include "common.h"
