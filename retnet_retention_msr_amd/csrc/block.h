@@ -59,8 +59,9 @@ struct ScanPlan {
 // for one another, and half as many of them, twice as long, wait less. Forward,
 // bf16, us at four and at eight: 512 units (8 x 8192 x 4096) 307 and 335, 256
 // units (4 x 8192 x 4096) 153 and 152, 32 units (65536 x 2048) 186 and 174, 4
-// units (32768 x 256) 29 and 21. Backward, log form: 256 units 257 and 311, 32
-// units 294 and 362, 1 unit (65536 x 64) 37 and 24. The tiles of a sequence are
+// units (32768 x 256) 29 and 21. Backward, log form: 240 units (15 x 4096 x
+// 1024) 130 and 132, 128 units 78 and 78, 32 units (65536 x 2048) 299 and 286,
+// 16 units (8192 x 1024) 31 and 25. The tiles of a sequence are
 // equally long: 130 tokens as two of three waves, not of four and one, 90 us
 // against 113 at 240 x 130 x 2048.
 // With many units a tile waits for its predecessor's state alone: it is mostly
@@ -88,8 +89,7 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
   }
   p.units = S * columns;
   p.wave_rows = p.vec == 1 ? kScanNarrowRows : backward && form == 0 ? kScanSigmoidBackRows : kScanRows;
-  const int64_t many = backward && form != 0 ? 16 : kScanManyUnits;
-  const int64_t most = p.units >= many ? kScanMaxWaves / 2 : kScanMaxWaves;
+  const int64_t most = p.units >= kScanManyUnits ? kScanMaxWaves / 2 : kScanMaxWaves;
   const int64_t waves = (static_cast<int64_t>(max_len) + p.wave_rows - 1) / p.wave_rows;
   const int64_t cut = (waves + most - 1) / most;
   p.waves = static_cast<int>((waves + cut - 1) / cut);

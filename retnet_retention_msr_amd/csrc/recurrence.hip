@@ -504,7 +504,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then. bf16, with the
 // fill: sigmoid form 8 x 8192 x 4096 600 us (5.4 TB/s), log form 4 x 8192 x
-// 4096 256 us (5.2 TB/s), 65536 x 2048 301 us (4.5 TB/s). Bounds of four waves
+// 4096 256 us (5.2 TB/s), 65536 x 2048 286 us (4.7 TB/s). Bounds of four waves
 // to a SIMD where the registers suffice: the log form, 252 us against 257; in
 // fp32 its four tensors of 32 tokens do not fit.
 template <typename T, int FORM, int V, int E, bool CACHED>
