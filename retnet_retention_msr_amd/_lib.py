@@ -60,6 +60,10 @@ class GnStruct(ctypes.Structure):
                 ("gate", ctypes.c_void_p)]
 
 
+# RETENTION_H_F32 of include/retention_block.h: added to a dtype, h alone is float32.
+H_F32 = 0x100
+
+
 class View(ctypes.Structure):
     """retention_view_t: a [B, H, N, d] tensor's address and its strides in elements."""
 

@@ -207,6 +207,14 @@ def _sequences(t, cu_seqlens, max_len):
     return _ints(B, H, N, d), ((S, H, d) if t.dim() == 4 else (S, d)), S, max_len
 
 
+def _h_dtype(t, name, dtype):
+    """The dtype of h, given as a tensor or a dtype (None: the inputs'): the inputs' or float32."""
+    h = dtype if t is None else t if isinstance(t, torch.dtype) else getattr(t, "dtype", dtype)
+    if h not in (dtype, torch.float32):
+        raise ValueError(f"{name} must be {dtype} or torch.float32, not {h}")
+    return h
+
+
 def _state_to_fill(t, name, shape, device):
     if t is True:
         return torch.empty(shape, dtype=torch.float32, device=device)
@@ -228,7 +236,7 @@ def _scan_bytes(S, dims, max_len, packed, code):
 
 
 def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: Union[bool, torch.Tensor] = False,
-                     cu_seqlens=None, max_len: Optional[int] = None, out=None, workspace=None):
+                     cu_seqlens=None, max_len: Optional[int] = None, out=None, workspace=None, out_dtype=None):
     """Gated linear recurrence over sequences, per channel. Returns (h, state_out or None).
 
     ``form`` "sigmoid": a = sigmoid(gate), h_t = a_t h_{t-1} + (1 - a_t) x_t;
@@ -236,7 +244,9 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     starts the state anew; above 0 only while the products of 256 tokens' decays
     stay in fp32's range). x and gate are [B, N, D] or [B, H, N, d]; states
     are fp32 [B, D] or [B, H, d]. ``state_out``: False (not produced), True
-    (allocate) or a tensor to fill (it may be ``state_in`` itself).
+    (allocate) or a tensor to fill (it may be ``state_in`` itself). h has x's
+    dtype, or float32 where ``out_dtype`` (or ``out``) is: the backward reads
+    h, and a bfloat16 one brings its rounding into grad_gate.
 
     Packed sequences: with ``cu_seqlens`` (device int32 [S + 1]) B is 1 and
     sequence s holds tokens cu_seqlens[s] up to cu_seqlens[s + 1]; states are
@@ -249,13 +259,15 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     gate_view, code = like.view(gate, "gate"), _form(form)
     dims, states, S, max_len = _sequences(x, cu_seqlens, max_len)
     dev = like.device
-    out, out_view = like.output(out, "out")
+    h_dtype = _h_dtype(out if out_dtype is None else out_dtype, "out", like.dtype)
+    out, out_view = like.output(out, "out", h_dtype)
     if state_in is not None:
         _f32(state_in, "state_in", states, dev)
     state_out = _state_to_fill(state_out, "state_out", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence", x, _view(x), gate_view, out_view, *dims, code, dt, _ptr(state_in),
+    _call("retention_gated_recurrence", x, _view(x), gate_view, out_view, *dims, code,
+          dt if h_dtype is like.dtype else dt | _lib.H_F32, _ptr(state_in),
           _ptr(state_out), _ptr(cu_seqlens), S, max_len, _ptr(workspace), have)
     return out, state_out
 
@@ -265,8 +277,8 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
                               max_len: Optional[int] = None, grads=None, workspace=None):
     """Gradients of gated_recurrence for dL/dh = grad_h. Returns (grad_x, grad_gate, grad_state_in or None).
 
-    ``h`` is the forward call's output and ``state_in`` its starting state;
-    x may be None in the "log" form, which does not read it. ``grad_state_out``
+    ``h`` is the forward call's output (in the inputs' dtype or float32) and
+    ``state_in`` its starting state; x may be None in the "log" form, which does not read it. ``grad_state_out``
     is dL/d(final state) (fp32, None = 0); ``grad_state_in``: False (not
     produced), True (allocate) or a tensor to fill. ``grads``: optional
     preallocated (grad_x, grad_gate). Sequences as in the forward call. A
@@ -277,7 +289,9 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
     like = _Like(gate)
     if x is None and code == 0:
         raise ValueError("the sigmoid form needs x")
-    inputs = (like.view(grad_h, "grad_h"), None if x is None else like.view(x, "x"), _view(gate), like.view(h, "h"))
+    h_dtype = _h_dtype(h, "h", like.dtype)
+    inputs = (like.view(grad_h, "grad_h"), None if x is None else like.view(x, "x"), _view(gate),
+              like.view(h, "h", h_dtype))
     dims, states, S, max_len = _sequences(gate, cu_seqlens, max_len)
     dev = like.device
     if grads is None:
@@ -291,7 +305,8 @@ def gated_recurrence_backward(grad_h, x, gate, h, form: str = "sigmoid", state_i
     grad_state_in = _state_to_fill(grad_state_in, "grad_state_in", states, dev)
     nbytes = _scan_bytes(S, dims, max_len, cu_seqlens is not None, dt)
     workspace, have = _workspace(workspace, nbytes, dev)
-    _call("retention_gated_recurrence_backward", gate, *inputs, dx_view, dg_view, *dims, code, dt,
+    _call("retention_gated_recurrence_backward", gate, *inputs, dx_view, dg_view, *dims, code,
+          dt if h_dtype is like.dtype else dt | _lib.H_F32,
           _ptr(state_in), _ptr(grad_state_out), _ptr(grad_state_in), _ptr(cu_seqlens), S, max_len, _ptr(workspace),
           have)
     return grad_x, grad_gate, grad_state_in

@@ -108,6 +108,8 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
               static_cast<size_t>(columns) * p.slots * kScanChannels * (p.folds ? 12 : 4);
   return p;
 }
+// In the dtype of the launches over sequences: h is fp32, the rest of dtype.
+constexpr int kWideH = 0x100;
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,
                                    const Sequences& q, const float* state_in, float* state_out, void* workspace,
                                    hipStream_t stream);

@@ -20,6 +20,10 @@ constexpr int64_t kMaxThreads = int64_t{1} << 32;  // below which a launch's sta
 constexpr int64_t kMaxStepChannels = int64_t{1} << 30;
 constexpr int kMaxSequences = 1 << 20;
 
+static_assert(RETENTION_H_F32 == ret::kWideH, "the launchers' flag is the ABI's");
+int h_type(int dtype) { return dtype & RETENTION_H_F32 ? static_cast<int>(RET_F32) : dtype; }
+int base_type(int dtype) { return dtype & ~RETENTION_H_F32; }
+
 int status_of(hipError_t e) { return e == hipSuccess ? RET_OK : RET_ERR_HIP; }
 bool valid_dtype(int dtype) { return dtype == RET_F32 || dtype == RET_BF16; }
 int64_t elem_size(int dtype) { return dtype == RET_F32 ? 4 : 2; }
@@ -189,6 +193,7 @@ extern "C" {
 
 size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int N, int max_len, int packed, int d,
                                                   int dtype) {
+  dtype = base_type(dtype);
   if (sequences <= 0 || max_len <= 0 || d > kMaxChannels || (packed && sequences > kMaxSequences)) return 0;
   if (!packed && max_len != N) return 0;
   if (check_dims(packed ? 1 : sequences, H, N, d, dtype) != RET_OK) return 0;
@@ -202,6 +207,8 @@ int retention_gated_recurrence(const retention_view_t* x, const retention_view_t
                                size_t workspace_bytes, void* stream) {
   Ranges ranges;
   Sequences q;
+  const int given = dtype, h_dtype = h_type(dtype);
+  dtype = base_type(dtype);
   int st = check_sequences(B, H, N, d, form, dtype, cu_seqlens, sequences, max_len, workspace, workspace_bytes, &q,
                            &ranges);
   if (st != RET_OK) return st;
@@ -211,13 +218,13 @@ int retention_gated_recurrence(const retention_view_t* x, const retention_view_t
   ranges.input(r);
   if ((st = check_view(gate, B, H, N, d, dtype, true, false, &vg, &r)) != RET_OK) return st;
   ranges.input(r);
-  if ((st = check_view(h, B, H, N, d, dtype, true, true, &vh, &r)) != RET_OK) return st;
+  if ((st = check_view(h, B, H, N, d, h_dtype, true, true, &vh, &r)) != RET_OK) return st;
   ranges.output(r);
   if (far_tokens(vx) || far_tokens(vg) || far_tokens(vh)) return RET_ERR_UNSUPPORTED;
   st = check_states(state_in, state_out, static_cast<int64_t>(sequences) * H * d, &ranges);
   if (st != RET_OK) return st;
   if (ranges.clash()) return RET_ERR_INVALID_ARG;
-  return status_of(ret::launch_gated_recurrence(form, dtype, vx, vg, vh, q, state_in, state_out, workspace,
+  return status_of(ret::launch_gated_recurrence(form, given, vx, vg, vh, q, state_in, state_out, workspace,
                                                 static_cast<hipStream_t>(stream)));
 }
 
@@ -230,6 +237,8 @@ int retention_gated_recurrence_backward(const retention_view_t* grad_h, const re
                                         void* stream) {
   Ranges ranges;
   Sequences q;
+  const int given = dtype, h_dtype = h_type(dtype);
+  dtype = base_type(dtype);
   int st = check_sequences(B, H, N, d, form, dtype, cu_seqlens, sequences, max_len, workspace, workspace_bytes, &q,
                            &ranges);
   if (st != RET_OK) return st;
@@ -239,7 +248,8 @@ int retention_gated_recurrence_backward(const retention_view_t* grad_h, const re
   Range r;
   for (int i = 0; i < 4; ++i) {
     const bool required = i != 1 || form == RET_GATE_SIGMOID;
-    if ((st = check_view(given_in[i], B, H, N, d, dtype, required, false, &in[i], &r)) != RET_OK) return st;
+    st = check_view(given_in[i], B, H, N, d, i == 3 ? h_dtype : dtype, required, false, &in[i], &r);
+    if (st != RET_OK) return st;
     ranges.input(r);
   }
   for (int i = 0; i < 2; ++i) {
@@ -254,7 +264,7 @@ int retention_gated_recurrence_backward(const retention_view_t* grad_h, const re
   ranges.input(r);
   if ((st = check_states(grad_state_out, grad_state_in, states, &ranges)) != RET_OK) return st;
   if (ranges.clash()) return RET_ERR_INVALID_ARG;
-  return status_of(ret::launch_gated_recurrence_backward(form, dtype, in[0], in[1], in[2], in[3], out[0], out[1], q,
+  return status_of(ret::launch_gated_recurrence_backward(form, given, in[0], in[1], in[2], in[3], out[0], out[1], q,
                                                          state_in, grad_state_out, grad_state_in, workspace,
                                                          static_cast<hipStream_t>(stream)));
 }

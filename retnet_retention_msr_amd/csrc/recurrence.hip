@@ -36,6 +36,8 @@
 #include "gate.h"
 #include "pack.h"
 
+#include <type_traits>
+
 namespace ret {
 
 namespace {
@@ -382,7 +384,8 @@ __device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const 
 // those before it: 65536 x 2048 (32 units) 174 us (4.6 TB/s), 32768 x 256 (4)
 // 22 us (2.3 TB/s). Rows that are no multiple of a cache line move up to a
 // quarter more bytes than theirs: 4 x 7501 x 1001 fp32 87 us (4.1 TB/s).
-template <typename T, int FORM, int V, int E, bool CACHED>
+// TH is h's type: T, or fp32 for a backward that takes h without T's rounding.
+template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
 __global__ void __launch_bounds__(64 * kScanMaxWaves, 4)
 recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_in, float* state_out, ScanWords w,
                   uint32_t units, int tiles) {
@@ -480,22 +483,22 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
   scan_carry<V>(A, Y, y, w, p, row0 + rows >= len, state_in ? state_in + unit_state : nullptr,
                 state_out ? state_out + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
-  T* hr = row_of<T>(out, p.piece.b, p.h) + p.piece.first * out.sn;
+  TH* hr = row_of<TH>(out, p.piece.b, p.h) + p.piece.first * out.sn;
   if (full) {
-    T* hb = hr + (row0 + at.wave * E) * out.sn;
+    TH* hb = hr + (row0 + at.wave * E) * out.sn;
     const uint32_t ho = at.sub * R * static_cast<uint32_t>(out.sn) + at.start;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
-      store_channels<CACHED, T, V>(hb + i * out.sn + ho, y, at);
+      store_channels<CACHED, TH, V>(hb + i * out.sn + ho, y, at);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
-      if (t0 + i < len) store_channels<CACHED, T, V>(hr + (t0 + i) * out.sn + at.start, y, at);
+      if (t0 + i < len) store_channels<CACHED, TH, V>(hr + (t0 + i) * out.sn + at.start, y, at);
     }
   }
 }
@@ -507,8 +510,8 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // 4096 256 us (5.2 TB/s), 65536 x 2048 286 us (4.7 TB/s). Bounds of four waves
 // to a SIMD where the registers suffice: the log form, 252 us against 257; in
 // fp32 its four tensors of 32 tokens do not fit.
-template <typename T, int FORM, int V, int E, bool CACHED>
-__global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(T) == 2 ? 4 : 2)
+template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
+__global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(TH) == 2 ? 4 : 2)
 recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
                            const float* state_in, const float* grad_state_out, float* grad_state_in, ScanWords w,
                            uint32_t units, int tiles) {
@@ -520,21 +523,25 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   if (p.tile < 0) return;
   const ScanLane<V> at(p.slab, q.d);
   const int len = p.piece.len;
+  typedef Pack<TH, V> PH;
   auto row = [&](const View& v) { return row_of<T>(v, p.piece.b, p.h) + p.piece.first * v.sn; };
-  const T *dr = row(grad_h), *gr = row(gate), *hr = row(hv), *xr = FORM == 0 ? row(x) : nullptr;
+  const T *dr = row(grad_h), *gr = row(gate), *xr = FORM == 0 ? row(x) : nullptr;
+  const TH* hr = row_of<TH>(hv, p.piece.b, p.h) + p.piece.first * hv.sn;
 
-  typename P::raw xw[R], hw[R], gw[R], dw[R];
+  typename P::raw xw[R], gw[R], dw[R];
+  typename PH::raw hw[R];
   // A tile's tokens and the one before them all exist where row + rows < len.
   auto load = [&](int tile) {
     const int64_t t = static_cast<int64_t>(tile) * rows;  // below len
     if (t + rows < len) {
       const int64_t low = len - (t + at.wave * E + E);  // the wave's first row in memory
       const uint32_t lane_row = (V - 1 - at.sub) * R;
-      auto get = [&](const T* from, int64_t sn, typename P::raw (&to)[R], int64_t back) {
-        const T* base = from + (low - back) * sn;
+      auto get = [&](const auto* from, int64_t sn, auto (&to)[R], int64_t back) {
+        const auto* base = from + (low - back) * sn;
         const uint32_t o = lane_row * static_cast<uint32_t>(sn) + at.start;
 #pragma unroll
-        for (int i = 0; i < R; ++i) to[i] = P::load(base + (R - 1 - i) * sn + o);
+        for (int i = 0; i < R; ++i)
+          to[i] = Pack<std::remove_const_t<std::remove_pointer_t<decltype(from)>>, V>::load(base + (R - 1 - i) * sn + o);
       };
       get(gr, gate.sn, gw, 0);
       get(dr, grad_h.sn, dw, 0);
@@ -547,7 +554,7 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
         r = r > 0 ? r : 0;
         gw[i] = P::load(gr + r * gate.sn + at.start);
         dw[i] = P::load(dr + r * grad_h.sn + at.start);
-        hw[i] = P::load(hr + (r > 0 ? r - 1 : 0) * hv.sn + at.start);
+        hw[i] = PH::load(hr + (r > 0 ? r - 1 : 0) * hv.sn + at.start);
         if (FORM == 0) xw[i] = P::load(xr + r * x.sn + at.start);
       }
     }
@@ -615,7 +622,7 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   for (int i = 0; i < R; ++i) {
     const int64_t r = len - 1 - (t0 + i);
     float before[V], v[V], dx[V], dg[V];
-    P::unpack(hw[i], before);
+    PH::unpack(hw[i], before);
     if (FORM == 0) P::unpack(xw[i], v);
     if (!full && r == 0) {
 #pragma unroll
@@ -757,6 +764,8 @@ hipError_t scan_words(const ScanPlan& p, void* workspace, ScanWords* words, hipS
 hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const View& gate, const View& h,
                                    const Sequences& q, const float* state_in, float* state_out, void* workspace,
                                    hipStream_t stream) {
+  const bool wide_h = dtype & kWideH;
+  dtype &= ~kWideH;
   const ScanPlan p = plan_scan(q.S, q.H, q.N, q.max_len, q.cu != nullptr, q.d, dtype, false, form);
   ScanWords words;
   const hipError_t e = scan_words(p, workspace, &words, stream);
@@ -769,25 +778,29 @@ hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const Vie
   // to be in the Infinity Cache still, results past it leave them there (176 MB,
   // 10749 x 2728 bf16: 54 against 46; 240 MB, 2 x 20000 x 1001 bf16: 74 and 75).
   const int64_t size = dtype == 0 ? 4 : 2;
+  const int64_t h_size = wide_h ? 4 : size;
   const int64_t rows = int64_t{q.cu ? 1 : q.S} * q.H * q.N;
-  const bool cached = h.sn * size % 128 != 0 && 3 * rows * q.d * size > kScanCacheBytes;
-#define RET_SCAN(T, FORM, V, E, CACHED)                                                                \
-  recurrence_kernel<T, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(x, gate, h, q, state_in,        \
-                                                                       state_out, words,               \
-                                                                       static_cast<uint32_t>(p.units), \
-                                                                       static_cast<int>(p.tiles))
-#define RET_SCAN_VEC(T, FORM, V)                                     \
-  do {                                                               \
-    if (p.vec == V && cached) RET_SCAN(T, FORM, V, kScanRows, true); \
-    else if (p.vec == V) RET_SCAN(T, FORM, V, kScanRows, false);     \
-    else RET_SCAN(T, FORM, 1, kScanNarrowRows, true);                \
+  const bool cached = h.sn * h_size % 128 != 0 && rows * q.d * (2 * size + h_size) > kScanCacheBytes;
+#define RET_SCAN(T, TH, FORM, V, E, CACHED)                                                                \
+  recurrence_kernel<T, TH, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(x, gate, h, q, state_in,        \
+                                                                           state_out, words,               \
+                                                                           static_cast<uint32_t>(p.units), \
+                                                                           static_cast<int>(p.tiles))
+#define RET_SCAN_VEC(T, TH, FORM, V)                                     \
+  do {                                                                   \
+    if (p.vec == V && cached) RET_SCAN(T, TH, FORM, V, kScanRows, true); \
+    else if (p.vec == V) RET_SCAN(T, TH, FORM, V, kScanRows, false);     \
+    else RET_SCAN(T, TH, FORM, 1, kScanNarrowRows, true);                \
   } while (0)
   if (dtype == 0) {
-    if (form == 0) RET_SCAN_VEC(float, 0, 4);
-    else RET_SCAN_VEC(float, 1, 4);
+    if (form == 0) RET_SCAN_VEC(float, float, 0, 4);
+    else RET_SCAN_VEC(float, float, 1, 4);
+  } else if (wide_h) {
+    if (form == 0) RET_SCAN_VEC(uint16_t, float, 0, 8);
+    else RET_SCAN_VEC(uint16_t, float, 1, 8);
   } else {
-    if (form == 0) RET_SCAN_VEC(uint16_t, 0, 8);
-    else RET_SCAN_VEC(uint16_t, 1, 8);
+    if (form == 0) RET_SCAN_VEC(uint16_t, uint16_t, 0, 8);
+    else RET_SCAN_VEC(uint16_t, uint16_t, 1, 8);
   }
 #undef RET_SCAN_VEC
 #undef RET_SCAN
@@ -798,6 +811,8 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
                                             const View& h, const View& grad_x, const View& grad_gate,
                                             const Sequences& q, const float* state_in, const float* grad_state_out,
                                             float* grad_state_in, void* workspace, hipStream_t stream) {
+  const bool wide_h = dtype & kWideH;
+  dtype &= ~kWideH;
   const ScanPlan p = plan_scan(q.S, q.H, q.N, q.max_len, q.cu != nullptr, q.d, dtype, true, form);
   ScanWords words;
   const hipError_t e = scan_words(p, workspace, &words, stream);
@@ -810,22 +825,25 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
   // against 203, 4 x 19454 x 696 321 against 313).
   const int64_t size = dtype == 0 ? 4 : 2;
   const bool cached = grad_x.sn * size % 128 != 0 || grad_gate.sn * size % 128 != 0;
-#define RET_SCAN(T, FORM, V, E, CACHED)                                                                    \
-  recurrence_backward_kernel<T, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(                           \
+#define RET_SCAN(T, TH, FORM, V, E, CACHED)                                                                \
+  recurrence_backward_kernel<T, TH, FORM, V, E, CACHED><<<grid, block, 0, stream>>>(                       \
       grad_h, x, gate, h, grad_x, grad_gate, q, state_in, grad_state_out, grad_state_in, words,            \
       static_cast<uint32_t>(p.units), static_cast<int>(p.tiles))
-#define RET_SCAN_VEC(T, FORM, V, E)                                    \
+#define RET_SCAN_VEC(T, TH, FORM, V, E)                                \
   do {                                                                 \
-    if (p.vec == V && cached) RET_SCAN(T, FORM, V, E, true);           \
-    else if (p.vec == V) RET_SCAN(T, FORM, V, E, false);               \
-    else RET_SCAN(T, FORM, 1, kScanNarrowRows, true);                  \
+    if (p.vec == V && cached) RET_SCAN(T, TH, FORM, V, E, true);       \
+    else if (p.vec == V) RET_SCAN(T, TH, FORM, V, E, false);           \
+    else RET_SCAN(T, TH, FORM, 1, kScanNarrowRows, true);              \
   } while (0)
   if (dtype == 0) {
-    if (form == 0) RET_SCAN_VEC(float, 0, 4, kScanSigmoidBackRows);
-    else RET_SCAN_VEC(float, 1, 4, kScanRows);
+    if (form == 0) RET_SCAN_VEC(float, float, 0, 4, kScanSigmoidBackRows);
+    else RET_SCAN_VEC(float, float, 1, 4, kScanRows);
+  } else if (wide_h) {
+    if (form == 0) RET_SCAN_VEC(uint16_t, float, 0, 8, kScanSigmoidBackRows);
+    else RET_SCAN_VEC(uint16_t, float, 1, 8, kScanRows);
   } else {
-    if (form == 0) RET_SCAN_VEC(uint16_t, 0, 8, kScanSigmoidBackRows);
-    else RET_SCAN_VEC(uint16_t, 1, 8, kScanRows);
+    if (form == 0) RET_SCAN_VEC(uint16_t, uint16_t, 0, 8, kScanSigmoidBackRows);
+    else RET_SCAN_VEC(uint16_t, uint16_t, 1, 8, kScanRows);
   }
 #undef RET_SCAN_VEC
 #undef RET_SCAN

@@ -385,3 +385,29 @@ def test_residual_norm_backward_workspace_is_what_its_launch_fills(lib):
     assert f(1, 1 << 20, 4096, 1, 1) == 512 * 3 * 4096 * 4
     assert f(1, 1 << 16, 16384, 0, 1) == 256 * 3 * 16384 * 4
     assert f(1, 100, 4096, 1, 1) == 100 * 3 * 4096 * 4 and f(1, 100, 4096, 1, 0) == 0
+
+
+def test_h_may_be_float32_alone(lib):
+    """With the flag h's elements are four bytes, the others two: told by what h's bytes meet and by its alignment."""
+    wide = 1 | _lib.H_F32
+    n = 2 * 3 * 100 * 64  # values of h
+    assert recurrence(lib, dtype=wide, h=A[2] + 2) == INVALID
+    assert recurrence(lib, dtype=wide, h=A[1] - 4 * n + 4) == INVALID
+    assert recurrence(lib, dtype=_lib.H_F32 | 2) == INVALID and recurrence(lib, dtype=1 | 2 * _lib.H_F32) == INVALID
+    assert backward(lib, dtype=wide, dx=A[3] + 4 * n - 2) == INVALID
+    assert step(lib, dtype=wide) == INVALID and gnorm(lib, dtype=wide) == INVALID
+    f = lib.retention_gated_recurrence_workspace_bytes
+    assert f(1, 3, 60000, 60000, 0, 64, wide) == f(1, 3, 60000, 60000, 0, 64, 1) > 0
+    if SHIM:
+        assert recurrence(lib, dtype=wide) == recurrence(lib, dtype=wide, h=A[1] - 4 * n) == 0
+        assert recurrence(lib, dtype=1, h=A[1] - 2 * n) == 0
+        assert backward(lib, dtype=wide) == backward(lib, dtype=wide, dx=A[3] + 4 * n) == 0
+
+
+def test_the_dtype_of_h():
+    bf16, f32 = torch.bfloat16, torch.float32
+    assert block._h_dtype(None, "out", bf16) is bf16 and block._h_dtype(f32, "out", bf16) is f32
+    assert block._h_dtype(torch.zeros(1), "h", bf16) is f32 and block._h_dtype(torch.zeros(1), "h", f32) is f32
+    for bad, dtype in ((torch.zeros(1, dtype=bf16), f32), (torch.float64, f32), (torch.float16, bf16)):
+        with pytest.raises(ValueError, match="out must be"):
+            block._h_dtype(bad, "out", dtype)
