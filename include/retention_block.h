@@ -20,7 +20,8 @@
  *     sizes <= 0 and misaligned data; RET_ERR_UNSUPPORTED: sizes beyond the
  *     limits stated at each function.
  *   - Sums, statistics and states are held in fp32; results in the element
- *     type are rounded once, to nearest even.
+ *     type are rounded once, to nearest even. The last h of a sequence is its
+ *     final state, rounded.
  *   - Results do not depend on timing: calls with the same arguments on the
  *     same data give the same bits (no floating-point atomics).
  */

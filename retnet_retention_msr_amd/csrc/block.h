@@ -29,7 +29,13 @@ struct Sequences {
 // of `rows` tokens, one workgroup of `waves` waves of `wave_rows` tokens each.
 // With more than one tile the workspace holds, per unit, a ticket and, per
 // tile and channel, what the tile passes on (recurrence.hip). Lanes take `vec`
-// channels, 16 bytes of them, or one where the whole row is shorter.
+// channels, or one where the whole row is shorter: four of them, 16 bytes of
+// fp32 and 8 of bf16, and in bf16's backward eight. A lane then holds fewer
+// tokens, and more lanes' folds have to be joined (24 exchanges of three words
+// against 8): forward, bf16, us at four and at eight: 8 x 8192 x 4096 301 and
+// 305, 16 heads x 65536 x 128 179 and 185, 2 x 2048 x 2048 15.3 and 17.1. The
+// backward's six tensors in pieces of 8 bytes cost more than that: 655 at four
+// and 619 at eight (8 x 8192 x 4096, sigmoid form).
 constexpr int kScanChannels = 64;
 constexpr uint32_t kXcds = 8, kXcdUnits = 9;
 constexpr int kScanMaxWaves = 8;
@@ -80,7 +86,7 @@ inline uint32_t scan_round(uint32_t n) {
 inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, int dtype, bool backward, int form) {
   ScanPlan p{};
   p.waves = 1;
-  p.vec = dtype == 0 ? 4 : 8;
+  p.vec = dtype != 0 && backward ? 8 : 4;
   if (d < p.vec) p.vec = 1;
   const int64_t columns = static_cast<int64_t>(H) * ((d + kScanChannels - 1) / kScanChannels);
   if (columns > (int64_t{1} << 30)) {

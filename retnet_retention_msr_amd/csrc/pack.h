@@ -29,6 +29,7 @@ struct Pack<float, V> {
     for (int j = 0; j < V; ++j) r[j] = x[j];
     return r;
   }
+  static __device__ __forceinline__ raw all(float v) { return raw(v); }
   static __device__ __forceinline__ void store(float* p, const float (&x)[V]) {
     // Eight floats are two accesses, each of which fills half of the lines it
     // touches: these go through the caches (residual norm backward with an
@@ -46,6 +47,7 @@ struct Pack<float, 1> {
   typedef float raw;
   static __device__ __forceinline__ raw load(const float* p) { return *p; }
   static __device__ __forceinline__ void unpack(const raw& r, float (&x)[1]) { x[0] = r; }
+  static __device__ __forceinline__ raw all(float v) { return v; }
   static __device__ __forceinline__ void store(float* p, const float (&x)[1]) { *p = x[0]; }
   static __device__ __forceinline__ void keep(float* p, const float (&x)[1]) { *p = x[0]; }
 };
@@ -69,6 +71,7 @@ struct Pack<uint16_t, V> {
     for (int j = 0; j < V / 2; ++j) r[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
     return r;
   }
+  static __device__ __forceinline__ raw all(float v) { return raw(pack_bf16x2(v, v)); }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[V]) {
     __builtin_nontemporal_store(pack(x), reinterpret_cast<anywhere*>(p));
   }
@@ -82,6 +85,7 @@ struct Pack<uint16_t, 1> {
   typedef uint16_t raw;
   static __device__ __forceinline__ raw load(const uint16_t* p) { return *p; }
   static __device__ __forceinline__ void unpack(const raw& r, float (&x)[1]) { x[0] = bf16_to_f32(r); }
+  static __device__ __forceinline__ raw all(float v) { return f32_to_bf16(v); }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[1]) { *p = f32_to_bf16(x[0]); }
   static __device__ __forceinline__ void keep(uint16_t* p, const float (&x)[1]) { *p = f32_to_bf16(x[0]); }
 };

@@ -13,11 +13,16 @@
 // takes a tile of tokens of 64 channels, reads it once into registers and
 // writes its outputs once; what the tokens before it contribute reaches it
 // through a few words per tile:
-//   - a lane holds V neighbouring channels (one 16-byte access, whatever its
-//     alignment; where d is no multiple of V the last lane's is moved back to
+//   - a lane holds V neighbouring channels (one access, whatever its alignment; where d is no multiple of V the last lane's is moved back to
 //     end with the row) of R = E / V consecutive tokens, and folds them into
 //     (A, Y): y_out = A y_in + Y; pairs of folds join by
-//     (A1, Y1) then (A2, Y2) = (A1 A2, A2 Y1 + Y2);
+//     (A1, Y1) then (A2, Y2) = (A1 A2, A2 Y1 + Y2). Beside A goes M = A - 1,
+//     formed from the tokens' 1 - a without A's rounding, M = M1 + M2 A1:
+//     where A is near 1 the carry into the next tile is y_in + (M y_in + Y).
+//     With A itself, rounded in steps of 2^-24, a channel with a memory of L
+//     tokens would be off by up to L 2^-25 (1.7e-3 of h at 65536 tokens of
+//     constant gates, 2e-6 so). Within a tile the steps of A y_in + Y are few:
+//     a lane's A near 1 is taken from its M;
 //   - the V groups of lanes that hold the same channels at consecutive tokens
 //     join theirs through lane exchanges, the waves of the workgroup theirs
 //     through LDS;
@@ -62,13 +67,18 @@ __device__ __forceinline__ T* row_of(const View& v, int b, int h) {
   return reinterpret_cast<T*>(v.data) + b * v.sb + h * v.sh;
 }
 
+// The gate that gives a decay of 1.
+template <int FORM>
+constexpr float kKeepGate = FORM == 0 ? __builtin_inff() : 0.0f;
+
+// The decay of a gate value, and 1 less it.
 template <int FORM>
 __device__ __forceinline__ void gate_of(float g, float& a, float& c) {
   if (FORM == 0) {
     sigmoid_pair(g, a, c);
   } else {
     a = __builtin_amdgcn_exp2f(kLog2e * g);
-    c = 1.0f;
+    c = 1.0f - a;
   }
 }
 
@@ -78,7 +88,7 @@ __device__ __forceinline__ void gate_of(float g, float& a, float& c) {
 struct ScanWords {
   uint32_t* ticket;  // [units], from all ones up
   uint32_t* state;   // [columns][slots][64]: the state after the tile
-  uint64_t* fold;    // [columns][slots][64]: Y, A; null: states alone
+  uint64_t* fold;    // [columns][slots][64]: Y, decay_word(A, M); null: states alone
   int64_t slots;
 };
 
@@ -91,10 +101,20 @@ __device__ __forceinline__ void publish(uint32_t* at, float v) {
   const uint32_t w = __float_as_uint(v);
   __hip_atomic_store(at, w == ~0u ? 0x7fc00000u : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void publish(uint64_t* at, float A, float Y) {
-  uint64_t w = static_cast<uint64_t>(__float_as_uint(Y)) << 32 | __float_as_uint(A);
+__device__ __forceinline__ void publish(uint64_t* at, float m, float Y) {
+  uint64_t w = static_cast<uint64_t>(__float_as_uint(Y)) << 32 | __float_as_uint(m);
   if (w == ~uint64_t{0}) w = uint64_t{0x7fc00000u} << 32 | 0x7fc00000u;
   __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// A fold's A and M in one word: M, its sign bit set, for A from 1/2 to 1, and
+// else A, which has no sign.
+__device__ __forceinline__ float decay_word(float A, float M) {
+  return M >= -0.5f && M <= 0.0f ? -__builtin_fabsf(M) : A;
+}
+// A y + Y for such a word: near 1 the sum is rounded once, to y's steps.
+__device__ __forceinline__ float fold_on(float m, float Y, float y) {
+  return (__float_as_int(m) < 0 ? y : 0.0f) + fmaf(m, y, Y);
 }
 
 // The states of 64 channels (a lane each) before `tile` > 0, from the words of
@@ -112,7 +132,7 @@ constexpr int kAhead = 2;
 constexpr int kDepth = 32;
 constexpr int kPolls = 1 << 20;
 __device__ __forceinline__ float fold_on(uint64_t f, float y) {
-  return fmaf(__uint_as_float(static_cast<uint32_t>(f)), y, __uint_as_float(static_cast<uint32_t>(f >> 32)));
+  return fold_on(__uint_as_float(static_cast<uint32_t>(f)), __uint_as_float(static_cast<uint32_t>(f >> 32)), y);
 }
 typedef uint64_t Stash[kDepth][kScanChannels];
 
@@ -181,7 +201,8 @@ __device__ __forceinline__ float last_state(const uint32_t* state, int tile) {
 // last lanes of a row whose width is no multiple of V use the places before 0.
 constexpr int kPad = 8;
 struct ScanShared {
-  float2 fold[kScanMaxWaves][kPad + kScanChannels];  // the waves' folds, then in x the carry into each wave
+  float4 fold[kScanMaxWaves][kPad + kScanChannels];  // the waves' folds A, Y, M, then in x the carry into each wave
+  float after[kPad + kScanChannels];                 // the state after the sequence's last tile
   Stash stash;
   int tile;
 };
@@ -296,31 +317,45 @@ __device__ __forceinline__ int take_ticket(const ScanWords& w, int64_t unit, int
   return __builtin_amdgcn_readfirstlane(at);
 }
 
-// Joins the lanes' folds (A, Y) of the workgroup, gets the tile's carry and
+// Joins the lanes' folds (A, M, Y) of the workgroup, gets the tile's carry and
 // leaves in y the state before each lane's first token. `first` and `last` are
 // the states before the sequence (may be null) and after it (null: not
 // wanted), at this unit's channel 0; `left` how many channels there are.
-template <int V>
-__device__ __forceinline__ void scan_carry(float (&A)[V], float (&Y)[V], float (&y)[V], const ScanWords& w,
-                                           const ScanPlace& p, bool end, const float* first, float* last,
-                                           int left, const ScanLane<V>& at, ScanShared& shared) {
+template <int V, int K>
+__device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (&Y)[V], float (&y)[V],
+                                           const ScanWords& w, const ScanPlace& p, bool end, const float* first,
+                                           float* last, int left, const ScanLane<V>& at, ScanShared& shared) {
   constexpr int CG = kScanChannels / V;  // lanes side by side
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  // Inclusive over the V groups of lanes.
+#pragma unroll
+  for (int j = 0; j < V; ++j) A[j] = M[j] >= -0.5f ? 1.0f + M[j] : A[j];  // one rounding, not one a token
+  // Inclusive over the V groups of lanes, K channels at a time: the words on
+  // their way are registers (all of V at once spills).
 #pragma unroll
   for (int off = 1; off < V; off *= 2) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float A1 = __shfl_up(A[j], off * CG, 64), Y1 = __shfl_up(Y[j], off * CG, 64);
+    for (int j0 = 0; j0 < V; j0 += K) {
+      float A1[K], M1[K], Y1[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        A1[k] = __shfl_up(A[j0 + k], off * CG, 64);
+        M1[k] = __shfl_up(M[j0 + k], off * CG, 64);
+        Y1[k] = __shfl_up(Y[j0 + k], off * CG, 64);
+      }
       if (at.sub >= off) {
-        Y[j] = fmaf(A[j], Y1, Y[j]);
-        A[j] *= A1;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int j = j0 + k;
+          Y[j] = fmaf(A[j], Y1[k], Y[j]);
+          M[j] = fmaf(M[j], A1[k], M1[k]);
+          A[j] *= A1[k];
+        }
       }
     }
   }
   if (at.sub == V - 1) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) shared.fold[at.wave][at.word + j] = make_float2(A[j], Y[j]);
+    for (int j = 0; j < V; ++j) shared.fold[at.wave][at.word + j] = make_float4(A[j], Y[j], M[j], 0.0f);
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -330,12 +365,15 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&Y)[V], float (
   }
   lds_only_barrier();
   if (at.wave == 0) {  // a lane per channel
-    float TA = 1.0f, TY = 0.0f;
+    float TA = 1.0f, TM = 0.0f, TY = 0.0f;
+#pragma unroll 2  // more in flight spill where the backward holds four tensors
     for (int k = 0; k < waves; ++k) {
-      const float2 g = shared.fold[k][kPad + lane];
+      const float4 g = shared.fold[k][kPad + lane];
       TY = fmaf(g.x, TY, g.y);
+      TM = fmaf(g.z, TA, TM);
       TA *= g.x;
     }
+    const float m = decay_word(TA, TM);
     const int64_t word = p.slot0 * kScanChannels + lane;
     const int64_t here = word + static_cast<int64_t>(p.tile) * kScanChannels;
     float carry;
@@ -343,17 +381,22 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&Y)[V], float (
       carry = first && lane < left ? first[lane] : 0.0f;
     } else {
       if (w.fold) {
-        if (!end) publish(w.fold + here, TA, TY);
+        if (!end) publish(w.fold + here, m, TY);
         carry = look_back(w.fold + word, w.state + word, p.tile, shared.stash, lane);
       } else {
         carry = last_state(w.state + word, p.tile);
       }
     }
-    const float after = fmaf(TA, carry, TY);
-    if (!end) publish(w.state + here, after);
-    else if (last && lane < left) last[lane] = after;
+    const float after = fold_on(m, TY, carry);
+    if (end) {
+      shared.after[kPad + lane] = after;
+      if (last && lane < left) last[lane] = after;
+    } else {
+      publish(w.state + here, after);
+    }
+#pragma unroll 2
     for (int k = 0; k < waves; ++k) {
-      const float2 g = shared.fold[k][kPad + lane];
+      const float4 g = shared.fold[k][kPad + lane];
       shared.fold[k][kPad + lane].x = carry;
       carry = fmaf(g.x, carry, g.y);
     }
@@ -379,9 +422,9 @@ __device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const 
   }
 }
 
-// bf16, with the fill: 8 x 8192 x 4096 304 us (5.3 TB/s, a device copy of 1 GiB
-// 5.1), 4 x 8192 x 4096 150 us. With few units a tile waits for the slowest of
-// those before it: 65536 x 2048 (32 units) 174 us (4.6 TB/s), 32768 x 256 (4)
+// bf16, with the fill: 8 x 8192 x 4096 301 us (5.3 TB/s, a device copy of 1 GiB
+// 5.1), 4 x 8192 x 4096 154 us. With few units a tile waits for the slowest of
+// those before it: 65536 x 2048 (32 units) 184 us (4.4 TB/s), 32768 x 256 (4)
 // 22 us (2.3 TB/s). Rows that are no multiple of a cache line move up to a
 // quarter more bytes than theirs: 4 x 7501 x 1001 fp32 87 us (4.1 TB/s).
 // TH is h's type: T, or fp32 for a backward that takes h without T's rounding.
@@ -442,46 +485,32 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   const int64_t t0 = row0 + at.wave * E + at.sub * R;
   const bool full = row0 + rows <= len;
 
-  float a[R][V], b[R][V];
+  float a[R][V], b[R][V], A[V], M[V], Y[V], y[V];
+  if (!full) {  // tokens past the end: a = 1, x = 0
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t0 + i < len) continue;
+      gw[i] = P::all(kKeepGate<FORM>);
+      xw[i] = P::all(0.0f);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     P::unpack(gw[i], a[i]);
     P::unpack(xw[i], b[i]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (FORM == 0) {
-        float keep;
-        sigmoid_pair(a[i][j], a[i][j], keep);
-        b[i][j] *= keep;
-      } else {
-        a[i][j] = __builtin_amdgcn_exp2f(kLog2e * a[i][j]);
-      }
-    }
-  }
-  if (!full) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (t0 + i < len) continue;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        a[i][j] = 1.0f;
-        b[i][j] = 0.0f;
-      }
-    }
-  }
-  float A[V], Y[V], y[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    A[j] = a[0][j];
-    Y[j] = b[0][j];
-#pragma unroll
-    for (int i = 1; i < R; ++i) {
-      Y[j] = fmaf(a[i][j], Y[j], b[i][j]);
-      A[j] *= a[i][j];
+      float c;  // 1 - a
+      gate_of<FORM>(a[i][j], a[i][j], c);
+      if (FORM == 0) b[i][j] *= c;
+      M[j] = i ? fmaf(-c, A[j], M[j]) : -c;
+      A[j] = i ? A[j] * a[i][j] : a[i][j];
+      Y[j] = i ? fmaf(a[i][j], Y[j], b[i][j]) : b[i][j];
     }
   }
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
-  scan_carry<V>(A, Y, y, w, p, row0 + rows >= len, state_in ? state_in + unit_state : nullptr,
+  const bool end = row0 + rows >= len;
+  scan_carry<V, 4>(A, M, Y, y, w, p, end, state_in ? state_in + unit_state : nullptr,
                 state_out ? state_out + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
   TH* hr = row_of<TH>(out, p.piece.b, p.h) + p.piece.first * out.sn;
   if (full) {
@@ -501,15 +530,21 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
       if (t0 + i < len) store_channels<CACHED, TH, V>(hr + (t0 + i) * out.sn + at.start, y, at);
     }
   }
+  if (end && t0 < len && len <= t0 + R) {  // the last h is the final state, to the bit
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = shared.after[at.word + j];
+    store_channels<CACHED, TH, V>(hr + (len - 1) * out.sn + at.start, y, at);
+  }
 }
 
 // The same from the last token on: token t of the recurrence is row
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then. bf16, with the
-// fill: sigmoid form 8 x 8192 x 4096 600 us (5.4 TB/s), log form 4 x 8192 x
-// 4096 256 us (5.2 TB/s), 65536 x 2048 286 us (4.7 TB/s). Bounds of four waves
-// to a SIMD where the registers suffice: the log form, 252 us against 257; in
-// fp32 its four tensors of 32 tokens do not fit.
+// fill: sigmoid form 8 x 8192 x 4096 620 us (5.2 TB/s; 600 without M), log form
+// 4 x 8192 x 4096 258 us (5.2 TB/s), 65536 x 2048 284 us (4.7 TB/s). Bounds of
+// four waves to a SIMD where the registers suffice: the log form, 252 us
+// against 257; its three tensors of 32 tokens in fp32, or with an fp32 h, do
+// not fit.
 template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
 __global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(TH) == 2 ? 4 : 2)
 recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
@@ -575,53 +610,41 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   // which has more digits, and any other as it is.
   auto decay = [](float v) { return FORM == 0 && __float_as_int(v) < 0 ? 1.0f + v : v; };
   auto rest = [](float v) { return __float_as_int(v) < 0 ? -v : 1.0f - v; };
-  float a[R][V], dh[R][V];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    P::unpack(gw[i], a[i]);
-    P::unpack(dw[i], dh[i]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (FORM == 0) {
-        float keep, d;
-        sigmoid_pair(a[i][j], d, keep);
-        a[i][j] = d > 0.5f ? -keep : d;
-      } else {
-        a[i][j] = __builtin_amdgcn_exp2f(kLog2e * a[i][j]);
-      }
-    }
-  }
-  if (!full) {
+  float a[R][V], A[V], M[V], Y[V], y[V];
+  if (!full) {  // tokens past the end: a = 1, dh = 0
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t0 + i < len) continue;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        a[i][j] = FORM == 0 ? -0.0f : 1.0f;
-        dh[i][j] = 0.0f;
-      }
+      gw[i] = P::all(kKeepGate<FORM>);
+      dw[i] = P::all(0.0f);
     }
   }
-  float A[V], Y[V], y[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    A[j] = 1.0f;
-    Y[j] = 0.0f;
+  for (int i = 0; i < R; ++i) {
+    float dh[V];
+    P::unpack(gw[i], a[i]);
+    P::unpack(dw[i], dh);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float d = decay(a[i][j]);
-      Y[j] = d * (Y[j] + dh[i][j]);
-      A[j] *= d;
+    for (int j = 0; j < V; ++j) {
+      float d, c;  // the decay and 1 less it
+      gate_of<FORM>(a[i][j], d, c);
+      a[i][j] = FORM == 0 && d > 0.5f ? -c : d;
+      M[j] = i ? fmaf(-c, A[j], M[j]) : -c;
+      A[j] = i ? A[j] * d : d;
+      Y[j] = d * (i ? Y[j] + dh[j] : dh[j]);
     }
   }
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
-  scan_carry<V>(A, Y, y, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
+  scan_carry<V, 2>(A, M, Y, y, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
                 grad_state_in ? grad_state_in + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
   T *dxr = row(grad_x), *dgr = row(grad_gate);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t r = len - 1 - (t0 + i);
-    float before[V], v[V], dx[V], dg[V];
+    float before[V], v[V], dh[V], dx[V], dg[V];
+    // Unpacked again: the compiler would hold both, and spill.
+    if constexpr (sizeof(T) == 2 && V > 1) asm volatile("" : "+v"(dw[i]));
+    P::unpack(dw[i], dh);
     PH::unpack(hw[i], before);
     if (FORM == 0) P::unpack(xw[i], v);
     if (!full && r == 0) {
@@ -630,7 +653,7 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float d = decay(a[i][j]), u = dh[i][j] + y[j];
+      const float d = decay(a[i][j]), u = dh[j] + y[j];
       y[j] = d * u;
       if (FORM == 0) {
         dx[j] = rest(a[i][j]) * u;
@@ -704,9 +727,11 @@ step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int
       P::unpack(xw, v);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float a, keep;
-        gate_of<FORM>(g[j], a, keep);
-        now[j] = fmaf(a, now[j], keep * v[j]);
+        float a, c;
+        gate_of<FORM>(g[j], a, c);
+        if (FORM == 0) v[j] *= c;
+        // As fold_on(): over many steps a's own rounding would add up.
+        now[j] = fold_on(FORM == 0 && g[j] >= 0.0f ? -c : a, v[j], now[j]);
       }
       if (in) {
         T* o = row_of<T>(out, i, h) + start;
@@ -796,11 +821,11 @@ hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const Vie
     if (form == 0) RET_SCAN_VEC(float, float, 0, 4);
     else RET_SCAN_VEC(float, float, 1, 4);
   } else if (wide_h) {
-    if (form == 0) RET_SCAN_VEC(uint16_t, float, 0, 8);
-    else RET_SCAN_VEC(uint16_t, float, 1, 8);
+    if (form == 0) RET_SCAN_VEC(uint16_t, float, 0, 4);
+    else RET_SCAN_VEC(uint16_t, float, 1, 4);
   } else {
-    if (form == 0) RET_SCAN_VEC(uint16_t, uint16_t, 0, 8);
-    else RET_SCAN_VEC(uint16_t, uint16_t, 1, 8);
+    if (form == 0) RET_SCAN_VEC(uint16_t, uint16_t, 0, 4);
+    else RET_SCAN_VEC(uint16_t, uint16_t, 1, 4);
   }
 #undef RET_SCAN_VEC
 #undef RET_SCAN

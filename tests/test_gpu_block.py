@@ -852,3 +852,55 @@ def test_a_bf16_h_rounds_grad_gate_twice():
     narrow = off(ret.gated_recurrence(x.to(DEV), g.to(DEV), "log")[0])
     wide = off(ret.gated_recurrence(x.to(DEV), g.to(DEV), "log", out_dtype=F32)[0])
     assert 1.13e-3 < wide < 2.26e-3 and narrow > 1.118 * wide
+
+
+# ---------------------------------------------------------------------------
+# Decays near 1
+
+# A rounding of the state per tile (of 64 tokens at least, in the backward of 32768 tokens 512 of them, 2^-24 each:
+# 3.1e-5), the decays' and the weights' own errors, (|g| + 8) 2^-24 of their distance from 1 (1.4e-6 at 16), and some 32
+# roundings within a tile (1.9e-6).
+LONG = 5e-5
+
+
+@pytest.mark.parametrize("B, N, D", [(1, 32768, 65), (256, 8192, 64)])
+def test_long_memories_of_the_sigmoid_form(B, N, D):
+    """Constant gates up to 16 (memories of 3000 to 9 million tokens) and a constant input, against the closed form
+    x (1 - a^t): the weights of the state and of the input add up to 1 however many tokens there are."""
+    _announce(f"long memories {B, N, D}")
+    t = np.arange(1, N + 1)
+    x = torch.full((1, 1, D), 0.7, device=DEV).expand(B, N, D)
+    v = float(x[0, 0, 0])
+    for g in (8.0, 10.0, 12.0, 14.0, 15.0, 16.0):
+        gate = torch.full((1, 1, D), g, device=DEV).expand(B, N, D)
+        rise = -np.expm1(-np.log1p(np.exp(-g)) * t)  # 1 - a^t
+        h, s = ret.gated_recurrence(x, gate, state_out=True)
+        dx, dg, ds = ret.gated_recurrence_backward(x, x, gate, h, grad_state_in=True)
+        assert bool((h == h[:1, :, :1]).all()) and bool((dx == dx[:1, :, :1]).all())
+        np.testing.assert_allclose(orc.f64(h[0, :, 0]), v * rise, rtol=LONG)
+        np.testing.assert_allclose(orc.f64(s[0, 0]), v * rise[-1], rtol=LONG)
+        np.testing.assert_allclose(orc.f64(dx[0, :, 0]), v * rise[::-1], rtol=LONG)
+        c = 1 / (1 + np.exp(g))
+        before = v * np.concatenate(([0.0], rise[:-1]))
+        np.testing.assert_allclose(orc.f64(dg[0, :, 0]), (1 - c) * (before - v) * v * rise[::-1], rtol=0, atol=3 * LONG * v * v)
+        np.testing.assert_allclose(orc.f64(ds[0, 0]), v * rise[-1] * (1 - c) / c, rtol=LONG)
+
+
+def test_steps_keep_a_state_that_equals_the_input():
+    """Gates from 0 up: a state that is the input stays it to the bit, however many steps are taken."""
+    _announce("steps at a fixed point")
+    g = torch.linspace(0, 24, 333, device=DEV).expand(2, 333).contiguous()
+    x = torch.stack((torch.full((333,), 0.7), torch.linspace(-3, 5, 333))).to(DEV)
+    state = x.clone()
+    for _ in range(2000):
+        h = ret.gated_recurrence_step(x, g, state)
+    assert torch.equal(state, x) and torch.equal(h, x)
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 65), (1, 40, 3), (3, 129, 64), (1, 5000, 72), (260, 300, 64)])
+def test_the_last_h_is_the_final_state(shape):
+    _announce(f"last h {shape}")
+    x, s0 = _randn(shape, 1).to(DEV), _randn(_states(shape), 2).to(DEV)
+    for form in ("sigmoid", "log"):
+        h, s1 = ret.gated_recurrence(x, _gate(shape, 3, F32, form).to(DEV), form, state_in=s0, state_out=True)
+        assert torch.equal(h[:, -1], s1)
