@@ -18,6 +18,15 @@ __device__ __forceinline__ void sigmoid_pair(float g, float& a, float& one_less)
   one_less = g < 0.0f ? 1.0f - a : e * a;
 }
 
+// e^g and 1 - e^g. Near 0 the difference is the series' own, g (1 + g / 2 (1 +
+// g / 3 (1 + g / 4))), whose next term is below g^4 / 120, 2^-22.9 of it at
+// 1/16: 1 - a would have a's rounding, 2^-24 / |g| of it.
+__device__ __forceinline__ void exp_pair(float g, float& a, float& one_less) {
+  a = __builtin_amdgcn_exp2f(kLog2e * g);
+  const float series = fmaf(fmaf(fmaf(g, 1.0f / 24, 1.0f / 6), g, 0.5f), g, 1.0f);
+  one_less = __builtin_fabsf(g) < 0.0625f ? -g * series : 1.0f - a;
+}
+
 // Workgroup barrier that orders LDS accesses only: outstanding global loads
 // and stores stay in flight across it.
 __device__ __forceinline__ void lds_only_barrier() {

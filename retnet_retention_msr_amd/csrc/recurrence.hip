@@ -74,11 +74,36 @@ constexpr float kKeepGate = FORM == 0 ? __builtin_inff() : 0.0f;
 // The decay of a gate value, and 1 less it.
 template <int FORM>
 __device__ __forceinline__ void gate_of(float g, float& a, float& c) {
+  if (FORM == 0) sigmoid_pair(g, a, c);
+  else exp_pair(g, a, c);
+}
+
+// A token's decay a, in the sigmoid form with 1 - a in c.
+template <int FORM>
+__device__ __forceinline__ void token_decay(float g, float& a, float& c) {
+  if (FORM == 0) sigmoid_pair(g, a, c);
+  else a = __builtin_amdgcn_exp2f(kLog2e * g);
+}
+// A lane's A and M with its token i. In the log form A is the sum of the gates
+// until lane_decays(): one exponential and one series a lane, not one a token.
+template <int FORM>
+__device__ __forceinline__ void lane_decay(int i, float g, float a, float c, float& A, float& M) {
   if (FORM == 0) {
-    sigmoid_pair(g, a, c);
+    M = i ? fmaf(-c, A, M) : -c;
+    A = i ? A * a : a;
   } else {
-    a = __builtin_amdgcn_exp2f(kLog2e * g);
-    c = 1.0f - a;
+    A = i ? A + g : g;
+  }
+}
+template <int FORM, int V>
+__device__ __forceinline__ void lane_decays(float (&A)[V], float (&M)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (FORM == 1) {
+      exp_pair(A[j], A[j], M[j]);
+      M[j] = -M[j];
+    }
+    A[j] = M[j] >= -0.5f ? 1.0f + M[j] : A[j];  // one rounding, not one a token
   }
 }
 
@@ -327,8 +352,6 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
                                            float* last, int left, const ScanLane<V>& at, ScanShared& shared) {
   constexpr int CG = kScanChannels / V;  // lanes side by side
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-#pragma unroll
-  for (int j = 0; j < V; ++j) A[j] = M[j] >= -0.5f ? 1.0f + M[j] : A[j];  // one rounding, not one a token
   // Inclusive over the V groups of lanes, K channels at a time: the words on
   // their way are registers (all of V at once spills).
 #pragma unroll
@@ -500,14 +523,15 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
     P::unpack(xw[i], b[i]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float c;  // 1 - a
-      gate_of<FORM>(a[i][j], a[i][j], c);
+      const float g = a[i][j];
+      float c;
+      token_decay<FORM>(g, a[i][j], c);
       if (FORM == 0) b[i][j] *= c;
-      M[j] = i ? fmaf(-c, A[j], M[j]) : -c;
-      A[j] = i ? A[j] * a[i][j] : a[i][j];
+      lane_decay<FORM>(i, g, a[i][j], c, A[j], M[j]);
       Y[j] = i ? fmaf(a[i][j], Y[j], b[i][j]) : b[i][j];
     }
   }
+  lane_decays<FORM>(A, M);
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
   const bool end = row0 + rows >= len;
   scan_carry<V, 4>(A, M, Y, y, w, p, end, state_in ? state_in + unit_state : nullptr,
@@ -626,14 +650,15 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
     P::unpack(dw[i], dh);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float d, c;  // the decay and 1 less it
-      gate_of<FORM>(a[i][j], d, c);
+      const float g = a[i][j];
+      float d, c;
+      token_decay<FORM>(g, d, c);
+      lane_decay<FORM>(i, g, d, c, A[j], M[j]);
       a[i][j] = FORM == 0 && d > 0.5f ? -c : d;
-      M[j] = i ? fmaf(-c, A[j], M[j]) : -c;
-      A[j] = i ? A[j] * d : d;
       Y[j] = d * (i ? Y[j] + dh[j] : dh[j]);
     }
   }
+  lane_decays<FORM>(A, M);
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
   scan_carry<V, 2>(A, M, Y, y, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
                 grad_state_in ? grad_state_in + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
@@ -731,7 +756,7 @@ step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int
         gate_of<FORM>(g[j], a, c);
         if (FORM == 0) v[j] *= c;
         // As fold_on(): over many steps a's own rounding would add up.
-        now[j] = fold_on(FORM == 0 && g[j] >= 0.0f ? -c : a, v[j], now[j]);
+        now[j] = fold_on(decay_word(a, -c), v[j], now[j]);
       }
       if (in) {
         T* o = row_of<T>(out, i, h) + start;

@@ -904,3 +904,38 @@ def test_the_last_h_is_the_final_state(shape):
     for form in ("sigmoid", "log"):
         h, s1 = ret.gated_recurrence(x, _gate(shape, 3, F32, form).to(DEV), form, state_in=s0, state_out=True)
         assert torch.equal(h[:, -1], s1)
+
+
+@pytest.mark.parametrize("B, N, D", [(1, 32768, 65), (256, 8192, 64)])
+def test_long_memories_of_the_log_form(B, N, D):
+    """Constant gates down to -1e-6 and a constant input, against the closed form x (1 - a^t) / (1 - a)."""
+    _announce(f"long memories, log form {B, N, D}")
+    t = np.arange(1, N + 1)
+    x = torch.full((1, 1, D), 0.7, device=DEV).expand(B, N, D)
+    v = float(x[0, 0, 0])
+    for g in (-0.1, -1e-2, -1e-3, -1e-4, -1e-5, -1e-6):
+        gate = torch.full((1, 1, D), g, device=DEV).expand(B, N, D)
+        g = float(gate[0, 0, 0])
+        want = v * np.expm1(g * t) / np.expm1(g)
+        h, s = ret.gated_recurrence(x, gate, "log", state_out=True)
+        dx, dg, ds = ret.gated_recurrence_backward(x, x, gate, h, "log", grad_state_in=True)
+        assert bool((h == h[:1, :, :1]).all()) and bool((dx == dx[:1, :, :1]).all())
+        np.testing.assert_allclose(orc.f64(h[0, :, 0]), want, rtol=LONG)
+        np.testing.assert_allclose(orc.f64(s[0, 0]), want[-1], rtol=LONG)
+        np.testing.assert_allclose(orc.f64(dx[0, :, 0]), want[::-1], rtol=LONG)
+        before = np.concatenate(([0.0], want[:-1]))
+        np.testing.assert_allclose(orc.f64(dg[0, :, 0]), np.exp(g) * before * want[::-1], rtol=3 * LONG)
+        np.testing.assert_allclose(orc.f64(ds[0, 0]), np.exp(g) * want[-1], rtol=LONG)
+
+
+def test_log_steps_keep_a_state_that_the_input_sustains():
+    """Where x is (1 - a) times the state, the state stays: what x's rounding and 1 - a's leave, a few 2^-24 of x, is
+    below half a step of a state 16 times as large or more."""
+    _announce("log steps at a fixed point")
+    g = -torch.logspace(-7, -1.5, 333, device=DEV).expand(2, 333).contiguous()
+    state = torch.stack((torch.full((333,), 0.7), torch.linspace(-3, 5, 333))).to(DEV)
+    x = (-torch.expm1(g.double()) * state.double()).float()
+    keep = state.clone()
+    for _ in range(2000):
+        h = ret.gated_recurrence_step(x, g, state, "log")
+    assert torch.equal(state, keep) and torch.equal(h, keep)
