@@ -445,10 +445,10 @@ __device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const 
   }
 }
 
-// bf16, with the fill: 8 x 8192 x 4096 301 us (5.3 TB/s, a device copy of 1 GiB
-// 5.1), 4 x 8192 x 4096 154 us. With few units a tile waits for the slowest of
-// those before it: 65536 x 2048 (32 units) 184 us (4.4 TB/s), 32768 x 256 (4)
-// 22 us (2.3 TB/s). Rows that are no multiple of a cache line move up to a
+// bf16, with the fill: 8 x 8192 x 4096 299 us (5.4 TB/s, a device copy of 1 GiB
+// 5.1), 4 x 8192 x 4096 151 us. With few units a tile waits for the slowest of
+// those before it: 65536 x 2048 (32 units) 182 us (4.4 TB/s), 32768 x 256 (4)
+// 23 us (2.2 TB/s). Rows that are no multiple of a cache line move up to a
 // quarter more bytes than theirs: 4 x 7501 x 1001 fp32 87 us (4.1 TB/s).
 // TH is h's type: T, or fp32 for a backward that takes h without T's rounding.
 template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
@@ -475,10 +475,10 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
       const uint32_t xo = at.sub * R * static_cast<uint32_t>(x.sn) + at.start;
       const uint32_t go = at.sub * R * static_cast<uint32_t>(gate.sn) + at.start;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        gw[i] = P::load(gb + i * gate.sn + go);
-        xw[i] = P::load(xb + i * x.sn + xo);
-      }
+      for (int i = 0; i < R; ++i) gw[i] = P::load(gb + i * gate.sn + go);
+      __builtin_amdgcn_sched_barrier(0);  // gates first: 299 us at 8 x 8192 x 4096 against 301
+#pragma unroll
+      for (int i = 0; i < R; ++i) xw[i] = P::load(xb + i * x.sn + xo);
     } else {  // tokens past the end read the last one
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -564,7 +564,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // The same from the last token on: token t of the recurrence is row
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then. bf16, with the
-// fill: sigmoid form 8 x 8192 x 4096 620 us (5.2 TB/s; 600 without M), log form
+// fill: sigmoid form 8 x 8192 x 4096 610 us (5.3 TB/s; 601 without M), log form
 // 4 x 8192 x 4096 258 us (5.2 TB/s), 65536 x 2048 284 us (4.7 TB/s). Bounds of
 // four waves to a SIMD where the registers suffice: the log form, 252 us
 // against 257; its three tensors of 32 tokens in fp32, or with an fp32 h, do
@@ -603,7 +603,11 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
           to[i] = Pack<std::remove_const_t<std::remove_pointer_t<decltype(from)>>, V>::load(base + (R - 1 - i) * sn + o);
       };
       get(gr, gate.sn, gw, 0);
+      // In the order they are needed in: 610 us at 8 x 8192 x 4096 in the sigmoid
+      // form, 619 in the compiler's own.
+      __builtin_amdgcn_sched_barrier(0);
       get(dr, grad_h.sn, dw, 0);
+      __builtin_amdgcn_sched_barrier(0);
       get(hr, hv.sn, hw, 1);
       if (FORM == 0) get(xr, x.sn, xw, 0);
     } else {
