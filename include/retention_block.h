@@ -64,7 +64,10 @@ enum retention_gate_form {
  *   RET_GATE_SIGMOID:  h_t = a_t h_{t-1} + (1 - a_t) x_t
  *   RET_GATE_LOG:      h_t = a_t h_{t-1} + x_t
  * with h_{-1} = state_in (fp32 [sequences, H, d], NULL: zeros). A gate of -inf
- * gives a = 0: the state starts anew at that token. state_out (fp32
+ * (a = 0) starts the state anew at that token whatever it holds before, NaN and
+ * infinities included, and one of +inf in the sigmoid form (a = 1) keeps it
+ * whatever x holds. Behind any other x, gate or state that is not finite h is
+ * not finite either, infinite or NaN, up to the next gate of -inf. state_out (fp32
  * [sequences, H, d], NULL: not written) receives the last h in fp32 and may be
  * state_in itself. x, gate and h are [B, H, N, d].
  *
@@ -102,6 +105,8 @@ int retention_gated_recurrence(const retention_view_t* x, const retention_view_t
  *   RET_GATE_SIGMOID: grad_x = (1 - a) u, grad_gate = a (1 - a) (h_{t-1} - x_t) u
  *   RET_GATE_LOG:     grad_x = u,         grad_gate = a h_{t-1} u
  *   grad_state_in = a_0 u_0 (fp32; NULL: not written; may be grad_state_out)
+ * At a gate of -inf grad_gate and what goes on to the tokens before are 0, at
+ * one of +inf in the sigmoid form grad_x and grad_gate, whatever x, h and u hold.
  * h is the forward call's output and state_in its starting state (NULL:
  * zeros); h_{t-1} is read from them, so a bf16 h brings its rounding into
  * grad_gate (RETENTION_H_F32 keeps it out). x may
@@ -118,7 +123,8 @@ int retention_gated_recurrence_backward(const retention_view_t* grad_h, const re
 
 /*
  * One token of the recurrence for B rows: h_b = a_b s + (1 - a_b) x_b (or
- * + x_b in the log form), s <- h_b, with s the row's state. x, gate and h are
+ * + x_b in the log form), s <- h_b, with s the row's state. Gates of -inf and
+ * +inf as over sequences: a slot of any contents is reset by -inf. x, gate and h are
  * [B, H, 1, d]; states is fp32 [nstates, H, d], contiguous. Row b's state is
  * states[b] (nstates >= B) or, with slots (DEVICE int32 [B]), states[slots[b]].
  * A row whose slot is outside [0, nstates) is idle: its h is not written. Rows

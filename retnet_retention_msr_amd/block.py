@@ -240,9 +240,10 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     """Gated linear recurrence over sequences, per channel. Returns (h, state_out or None).
 
     ``form`` "sigmoid": a = sigmoid(gate), h_t = a_t h_{t-1} + (1 - a_t) x_t;
-    "log": a = exp(gate), h_t = a_t h_{t-1} + x_t (gate <= 0 for a decay; -inf
-    starts the state anew; above 0 only while the products of 256 tokens' decays
-    stay in fp32's range). x and gate are [B, N, D] or [B, H, N, d]; states
+    "log": a = exp(gate), h_t = a_t h_{t-1} + x_t (gate <= 0 for a decay; above
+    0 only while the products of 256 tokens' decays stay in fp32's range). A
+    gate of -inf starts the state anew, whatever it holds, and one of +inf in
+    the sigmoid form keeps it, whatever x holds. x and gate are [B, N, D] or [B, H, N, d]; states
     are fp32 [B, D] or [B, H, d]. ``state_out``: False (not produced), True
     (allocate) or a tensor to fill (it may be ``state_in`` itself). h has x's
     dtype, or float32 where ``out_dtype`` (or ``out``) is: the backward reads

@@ -34,6 +34,13 @@
 //     and tile 0 waits for none;
 //   - each lane then runs its tokens again from its carry, which is in order
 //     and in fp32, and rounds its outputs once.
+// A gate of -inf (a reset) forgets the state before it whatever it holds, and
+// one of +inf in the sigmoid form passes over whatever x holds, where the
+// formulas' products have 0 times infinity or NaN. A wave in which a lane's A is
+// not above 0, or its Y not finite, takes its tokens a second time, looking at
+// each (`special`); the others are spared that: their tokens have neither. A
+// fold with a reset in it is marked by M = NaN with A = 0; a decay that is 0 in
+// fp32 alone is no reset, and an infinite state stays infinite or becomes NaN.
 // Published words hold their own "not there yet" value (all ones, written by
 // scan_fill_kernel before each launch, 1 to 6 us), so one relaxed access is
 // enough.
@@ -84,6 +91,10 @@ __device__ __forceinline__ void token_decay(float g, float& a, float& c) {
   if (FORM == 0) sigmoid_pair(g, a, c);
   else a = __builtin_amdgcn_exp2f(kLog2e * g);
 }
+// In a special wave: 0 is kept for resets.
+__device__ __forceinline__ float mark_token(float g, float a) {
+  return a == 0.0f && g != -__builtin_inff() ? __uint_as_float(1u) : a;
+}
 // A lane's A and M with its token i. In the log form A is the sum of the gates
 // until lane_decays(): one exponential and one series a lane, not one a token.
 template <int FORM>
@@ -105,6 +116,25 @@ __device__ __forceinline__ void lane_decays(float (&A)[V], float (&M)[V]) {
     }
     A[j] = M[j] >= -0.5f ? 1.0f + M[j] : A[j];  // one rounding, not one a token
   }
+}
+// Marks the channels whose bit is set in `resets`.
+template <int V>
+__device__ __forceinline__ void mark_resets(uint32_t resets, float (&A)[V], float (&M)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (!(resets >> j & 1)) continue;
+    A[j] = 0.0f;
+    M[j] = __builtin_nanf("");
+  }
+}
+__device__ __forceinline__ bool resets(float A, float M) { return A == 0.0f && M != M; }
+__device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
+// Whether a lane of the wave has a fold that needs the careful way, or `odd`.
+template <int V>
+__device__ __forceinline__ bool wave_special(const float (&A)[V], const float (&Y)[V], bool odd) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) odd |= !(A[j] > 0.0f) | !finite(Y[j]);
+  return __any(odd);
 }
 
 // The workspace of a launch with more than one tile. A column is a head's slab;
@@ -133,13 +163,16 @@ __device__ __forceinline__ void publish(uint64_t* at, float m, float Y) {
 }
 
 // A fold's A and M in one word: M, its sign bit set, for A from 1/2 to 1, and
-// else A, which has no sign.
+// else A, which has no sign: 0 for a reset, and where a product of decays above
+// 0 has become 0 the least number above it, so that an infinite state stays
+// infinite.
 __device__ __forceinline__ float decay_word(float A, float M) {
-  return M >= -0.5f && M <= 0.0f ? -__builtin_fabsf(M) : A;
+  const float far = A == 0.0f && !resets(A, M) ? __uint_as_float(1u) : A;
+  return M >= -0.5f && M <= 0.0f ? -__builtin_fabsf(M) : far;
 }
 // A y + Y for such a word: near 1 the sum is rounded once, to y's steps.
 __device__ __forceinline__ float fold_on(float m, float Y, float y) {
-  return (__float_as_int(m) < 0 ? y : 0.0f) + fmaf(m, y, Y);
+  return (__float_as_int(m) < 0 ? y : 0.0f) + fmaf(m, m == 0.0f ? 0.0f : y, Y);
 }
 
 // The states of 64 channels (a lane each) before `tile` > 0, from the words of
@@ -347,38 +380,47 @@ __device__ __forceinline__ int take_ticket(const ScanWords& w, int64_t unit, int
 // the states before the sequence (may be null) and after it (null: not
 // wanted), at this unit's channel 0; `left` how many channels there are.
 template <int V, int K>
-__device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (&Y)[V], float (&y)[V],
+__device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (&Y)[V], float (&y)[V], bool special,
                                            const ScanWords& w, const ScanPlace& p, bool end, const float* first,
                                            float* last, int left, const ScanLane<V>& at, ScanShared& shared) {
   constexpr int CG = kScanChannels / V;  // lanes side by side
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   // Inclusive over the V groups of lanes, K channels at a time: the words on
   // their way are registers (all of V at once spills).
+  auto join = [&](auto careful) {
 #pragma unroll
-  for (int off = 1; off < V; off *= 2) {
+    for (int off = 1; off < V; off *= 2) {
 #pragma unroll
-    for (int j0 = 0; j0 < V; j0 += K) {
-      float A1[K], M1[K], Y1[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        A1[k] = __shfl_up(A[j0 + k], off * CG, 64);
-        M1[k] = __shfl_up(M[j0 + k], off * CG, 64);
-        Y1[k] = __shfl_up(Y[j0 + k], off * CG, 64);
-      }
-      if (at.sub >= off) {
+      for (int j0 = 0; j0 < V; j0 += K) {
+        float A1[K], M1[K], Y1[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const int j = j0 + k;
-          Y[j] = fmaf(A[j], Y1[k], Y[j]);
-          M[j] = fmaf(M[j], A1[k], M1[k]);
-          A[j] *= A1[k];
+          A1[k] = __shfl_up(A[j0 + k], off * CG, 64);
+          M1[k] = __shfl_up(M[j0 + k], off * CG, 64);
+          Y1[k] = __shfl_up(Y[j0 + k], off * CG, 64);
+        }
+        if (at.sub >= off) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int j = j0 + k;
+            if (careful && resets(A[j], M[j])) continue;
+            Y[j] = fmaf(A[j], Y1[k], Y[j]);
+            M[j] = fmaf(M[j], A1[k], M1[k]);
+            A[j] *= A1[k];
+          }
         }
       }
     }
-  }
+  };
+  if (special) join(std::true_type());
+  else join(std::false_type());
   if (at.sub == V - 1) {
 #pragma unroll
     for (int j = 0; j < V; ++j) shared.fold[at.wave][at.word + j] = make_float4(A[j], Y[j], M[j], 0.0f);
+  }
+  if (special) {  // M is not passed on: a reset is -0 from here
+#pragma unroll
+    for (int j = 0; j < V; ++j) A[j] = resets(A[j], M[j]) ? -0.0f : A[j];
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -395,6 +437,17 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
       TY = fmaf(g.x, TY, g.y);
       TM = fmaf(g.z, TA, TM);
       TA *= g.x;
+    }
+    const bool tile_special = __any(!(TA > 0.0f) | !finite(TY));
+    if (tile_special) {
+      TA = 1.0f;
+      TY = 0.0f;
+#pragma unroll 1
+      for (int k = 0; k < waves; ++k) {
+        const float4 g = shared.fold[k][kPad + lane];
+        TY = resets(g.x, g.z) ? g.y : fmaf(g.x, TY, g.y);
+        TA = resets(g.x, g.z) ? 0.0f : TA * g.x;
+      }
     }
     const float m = decay_word(TA, TM);
     const int64_t word = p.slot0 * kScanChannels + lane;
@@ -417,16 +470,29 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
     } else {
       publish(w.state + here, after);
     }
+    if (tile_special) {
+#pragma unroll 1
+      for (int k = 0; k < waves; ++k) {
+        const float4 g = shared.fold[k][kPad + lane];
+        shared.fold[k][kPad + lane].x = carry;
+        carry = resets(g.x, g.z) ? g.y : fmaf(g.x, carry, g.y);
+      }
+    } else {
 #pragma unroll 2
-    for (int k = 0; k < waves; ++k) {
-      const float4 g = shared.fold[k][kPad + lane];
-      shared.fold[k][kPad + lane].x = carry;
-      carry = fmaf(g.x, carry, g.y);
+      for (int k = 0; k < waves; ++k) {
+        const float4 g = shared.fold[k][kPad + lane];
+        shared.fold[k][kPad + lane].x = carry;
+        carry = fmaf(g.x, carry, g.y);
+      }
     }
   }
   lds_only_barrier();
 #pragma unroll
   for (int j = 0; j < V; ++j) y[j] = fmaf(A[j], shared.fold[at.wave][at.word + j].x, Y[j]);
+  if (special) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = __float_as_uint(A[j]) == 1u << 31 ? Y[j] : y[j];
+  }
 }
 
 // Stores a lane's channels: all V, or the last V - shift of them. CACHED: not
@@ -445,10 +511,10 @@ __device__ __forceinline__ void store_channels(T* p, const float (&x)[V], const 
   }
 }
 
-// bf16, with the fill: 8 x 8192 x 4096 299 us (5.4 TB/s, a device copy of 1 GiB
-// 5.1), 4 x 8192 x 4096 151 us. With few units a tile waits for the slowest of
-// those before it: 65536 x 2048 (32 units) 182 us (4.4 TB/s), 32768 x 256 (4)
-// 23 us (2.2 TB/s). Rows that are no multiple of a cache line move up to a
+// bf16, with the fill: 8 x 8192 x 4096 301 us (5.4 TB/s, a device copy of 1 GiB
+// 5.1), 4 x 8192 x 4096 152 us. With few units a tile waits for the slowest of
+// those before it: 65536 x 2048 (32 units) 185 us (4.4 TB/s), 32768 x 256 (4)
+// 24 us (2.1 TB/s). Rows that are no multiple of a cache line move up to a
 // quarter more bytes than theirs: 4 x 7501 x 1001 fp32 87 us (4.1 TB/s).
 // TH is h's type: T, or fp32 for a backward that takes h without T's rounding.
 template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
@@ -509,35 +575,48 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   const bool full = row0 + rows <= len;
 
   float a[R][V], b[R][V], A[V], M[V], Y[V], y[V];
-  if (!full) {  // tokens past the end: a = 1, x = 0
+  auto fold = [&](auto careful) {
+    if (!full) {  // tokens past the end: a = 1, x = 0
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t0 + i < len) continue;
+        gw[i] = P::all(kKeepGate<FORM>);
+        xw[i] = P::all(0.0f);
+      }
+    }
+    uint32_t zero = 0;  // channels with a reset
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (t0 + i < len) continue;
-      gw[i] = P::all(kKeepGate<FORM>);
-      xw[i] = P::all(0.0f);
-    }
-  }
+      P::unpack(gw[i], a[i]);
+      P::unpack(xw[i], b[i]);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    P::unpack(gw[i], a[i]);
-    P::unpack(xw[i], b[i]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float g = a[i][j];
-      float c;
-      token_decay<FORM>(g, a[i][j], c);
-      if (FORM == 0) b[i][j] *= c;
-      lane_decay<FORM>(i, g, a[i][j], c, A[j], M[j]);
-      Y[j] = i ? fmaf(a[i][j], Y[j], b[i][j]) : b[i][j];
+      for (int j = 0; j < V; ++j) {
+        const float g = a[i][j];
+        float c;
+        token_decay<FORM>(g, a[i][j], c);
+        if (FORM == 0) b[i][j] = careful && c == 0.0f ? 0.0f : b[i][j] * c;
+        lane_decay<FORM>(i, g, a[i][j], c, A[j], M[j]);
+        if (careful) a[i][j] = mark_token(g, a[i][j]);
+        const bool reset = careful && a[i][j] == 0.0f;
+        if (reset) zero |= 1u << j;
+        Y[j] = i && !reset ? fmaf(a[i][j], Y[j], b[i][j]) : b[i][j];
+      }
     }
+    lane_decays<FORM>(A, M);
+    if (careful) mark_resets(zero, A, M);
+  };
+  fold(std::false_type());
+  const bool special = wave_special(A, Y, false);
+  if (special) {
+    load(p.tile);
+    fold(std::true_type());
   }
-  lane_decays<FORM>(A, M);
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
   const bool end = row0 + rows >= len;
-  scan_carry<V, 4>(A, M, Y, y, w, p, end, state_in ? state_in + unit_state : nullptr,
+  scan_carry<V, 4>(A, M, Y, y, special, w, p, end, state_in ? state_in + unit_state : nullptr,
                 state_out ? state_out + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
   TH* hr = row_of<TH>(out, p.piece.b, p.h) + p.piece.first * out.sn;
-  if (full) {
+  if (full && !special) {
     TH* hb = hr + (row0 + at.wave * E) * out.sn;
     const uint32_t ho = at.sub * R * static_cast<uint32_t>(out.sn) + at.start;
 #pragma unroll
@@ -550,7 +629,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[j] = fmaf(a[i][j], y[j], b[i][j]);
+      for (int j = 0; j < V; ++j) y[j] = a[i][j] == 0.0f ? b[i][j] : fmaf(a[i][j], y[j], b[i][j]);
       if (t0 + i < len) store_channels<CACHED, TH, V>(hr + (t0 + i) * out.sn + at.start, y, at);
     }
   }
@@ -564,8 +643,9 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // The same from the last token on: token t of the recurrence is row
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then. bf16, with the
-// fill: sigmoid form 8 x 8192 x 4096 610 us (5.3 TB/s; 601 without M), log form
-// 4 x 8192 x 4096 258 us (5.2 TB/s), 65536 x 2048 284 us (4.7 TB/s). Bounds of
+// fill: sigmoid form 8 x 8192 x 4096 622 us (5.2 TB/s; 601 without M and the
+// look for special waves), log form 4 x 8192 x 4096 262 us (5.1 TB/s), 65536 x
+// 2048 285 us (4.7 TB/s). Bounds of
 // four waves to a SIMD where the registers suffice: the log form, 252 us
 // against 257; its three tensors of 32 tokens in fp32, or with an fp32 h, do
 // not fit.
@@ -639,32 +719,50 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
   auto decay = [](float v) { return FORM == 0 && __float_as_int(v) < 0 ? 1.0f + v : v; };
   auto rest = [](float v) { return __float_as_int(v) < 0 ? -v : 1.0f - v; };
   float a[R][V], A[V], M[V], Y[V], y[V];
-  if (!full) {  // tokens past the end: a = 1, dh = 0
+  float least = 1.0f;  // 1 - a of the lane's tokens: 0 where one is passed over
+  auto fold = [&](auto careful) {
+    if (!full) {  // tokens past the end: a = 1, dh = 0
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t0 + i < len) continue;
+        gw[i] = P::all(kKeepGate<FORM>);
+        dw[i] = P::all(0.0f);
+      }
+    }
+    uint32_t zero = 0;  // channels with a reset
+    float last[V];      // the decay of the token before; Y is the gradient of its h until the end
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (t0 + i < len) continue;
-      gw[i] = P::all(kKeepGate<FORM>);
-      dw[i] = P::all(0.0f);
-    }
-  }
+      float dh[V];
+      P::unpack(gw[i], a[i]);
+      P::unpack(dw[i], dh);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float dh[V];
-    P::unpack(gw[i], a[i]);
-    P::unpack(dw[i], dh);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float g = a[i][j];
-      float d, c;
-      token_decay<FORM>(g, d, c);
-      lane_decay<FORM>(i, g, d, c, A[j], M[j]);
-      a[i][j] = FORM == 0 && d > 0.5f ? -c : d;
-      Y[j] = d * (i ? Y[j] + dh[j] : dh[j]);
+      for (int j = 0; j < V; ++j) {
+        const float g = a[i][j];
+        float d, c;
+        token_decay<FORM>(g, d, c);
+        lane_decay<FORM>(i, g, d, c, A[j], M[j]);
+        if (FORM == 0) least = fminf(least, c);
+        if (careful) d = mark_token(g, d);
+        a[i][j] = FORM == 0 && d > 0.5f ? -c : d;
+        if (careful && d == 0.0f) zero |= 1u << j;
+        Y[j] = i && !(careful && last[j] == 0.0f) ? fmaf(last[j], Y[j], dh[j]) : dh[j];
+        last[j] = d;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) Y[j] = careful && last[j] == 0.0f ? 0.0f : last[j] * Y[j];
+    lane_decays<FORM>(A, M);
+    if (careful) mark_resets(zero, A, M);
+  };
+  fold(std::false_type());
+  const bool special = wave_special(A, Y, FORM == 0 && least == 0.0f);
+  if (special) {
+    load(p.tile);
+    fold(std::true_type());
   }
-  lane_decays<FORM>(A, M);
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
-  scan_carry<V, 2>(A, M, Y, y, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
+  scan_carry<V, 2>(A, M, Y, y, special, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
                 grad_state_in ? grad_state_in + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
   T *dxr = row(grad_x), *dgr = row(grad_gate);
 #pragma unroll
@@ -690,6 +788,17 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
       } else {
         dx[j] = u;
         dg[j] = before[j] * y[j];
+      }
+    }
+    // Resets, and tokens that are passed over: the products above may be 0 times
+    // what is not finite, be it h of the token before, x or u.
+    if (special) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool forgets = decay(a[i][j]) == 0.0f, keeps = FORM == 0 && rest(a[i][j]) == 0.0f;
+        y[j] = forgets ? 0.0f : y[j];
+        dx[j] = keeps ? 0.0f : dx[j];
+        dg[j] = forgets || keeps ? 0.0f : dg[j];
       }
     }
     if (full || r >= 0) {
@@ -758,9 +867,9 @@ step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int
       for (int j = 0; j < V; ++j) {
         float a, c;
         gate_of<FORM>(g[j], a, c);
-        if (FORM == 0) v[j] *= c;
+        if (FORM == 0) v[j] = c == 0.0f ? 0.0f : v[j] * c;
         // As fold_on(): over many steps a's own rounding would add up.
-        now[j] = fold_on(decay_word(a, -c), v[j], now[j]);
+        now[j] = fold_on(g[j] == -__builtin_inff() ? 0.0f : decay_word(a, -c), v[j], now[j]);
       }
       if (in) {
         T* o = row_of<T>(out, i, h) + start;

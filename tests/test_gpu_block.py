@@ -939,3 +939,140 @@ def test_log_steps_keep_a_state_that_the_input_sustains():
     for _ in range(2000):
         h = ret.gated_recurrence_step(x, g, state, "log")
     assert torch.equal(state, keep) and torch.equal(h, keep)
+
+
+# ---------------------------------------------------------------------------
+# Values that are not finite, and decays of 0 and 1
+
+
+def _bad_values():
+    return (float("inf"), -float("inf"), float("nan"))
+
+
+def _mixed(shape, form, seed):
+    """Gates between a memory of a few tokens and decays whose products over a tile leave fp32's range."""
+    if form == "sigmoid":
+        return _randn(shape, seed, F32, 4.0, 1.0)
+    return -torch.exp(_randn(shape, seed, F32, 2.0, -1.0))
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "log"])
+@pytest.mark.parametrize("B, N, D", [(1, 3000, 72), (260, 300, 64), (2, 200, 3), (1, 20, 9)])
+def test_a_reset_forgets_whatever_the_state_holds(B, N, D, form):
+    """A gate of -inf starts anew: behind it everything is as if the tokens and the state before it had been finite, to
+    the bit. From the bad value to the reset h is not finite; other channels and rows are untouched."""
+    _announce(f"reset {B, N, D} {form}")
+    x, g, s0, dh = _randn((B, N, D), 1), _mixed((B, N, D), form, 2), _randn((B, D), 3), _randn((B, N, D), 4)
+    dev = [t.to(DEV) for t in (x, g, s0, dh)]
+    for bad in _bad_values():
+        for at, reset in ((N // 3, N // 2), (N // 3, N // 3 + 1), (-1, 0), (-1, N - 1), (N - 2, N - 1)):  # -1: the state itself
+            gr = dev[1].clone()
+            gr[-1, reset, 1] = -float("inf")
+            clean = ret.gated_recurrence(dev[0], gr, form, state_in=dev[2], state_out=True)
+            xb, sb = dev[0].clone(), dev[2].clone()
+            if at >= 0:
+                xb[-1, at, 1] = bad
+            else:
+                sb[-1, 1] = bad
+            h, s1 = ret.gated_recurrence(xb, gr, form, state_in=sb, state_out=True)
+            hit = torch.zeros(B, N, D, dtype=torch.bool, device=DEV)
+            hit[-1, max(at, 0):reset, 1] = True
+            assert torch.equal(~h.isfinite(), hit), (bad, at, reset)
+            assert torch.equal(h[~hit], clean[0][~hit]) and torch.equal(s1, clean[1])
+            # The gradients of what lies behind the reset, and nothing that is not finite where the decay is 0.
+            want = ret.gated_recurrence_backward(dev[3], dev[0], gr, clean[0], form, state_in=dev[2], grad_state_in=True)
+            got = ret.gated_recurrence_backward(dev[3], xb, gr, h, form, state_in=sb, grad_state_in=True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+            bad_dg = torch.zeros_like(hit)
+            bad_dg[-1, max(at, 0):reset, 1] = True
+            assert torch.equal(got[1][~bad_dg], want[1][~bad_dg]) and float(got[1][-1, reset, 1]) == 0.0
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "log"])
+@pytest.mark.parametrize("B, N, D", [(1, 3000, 72), (260, 300, 64), (2, 200, 3)])
+def test_what_is_not_finite_stays_so_without_a_reset(B, N, D, form):
+    """Whatever the decays' products do, h does not turn finite again by itself; the gradient carried back likewise, and a
+    reset keeps it from the tokens before."""
+    _announce(f"not finite {B, N, D} {form}")
+    x, g, dh = (t.to(DEV) for t in (_randn((B, N, D), 1), _mixed((B, N, D), form, 2), _randn((B, N, D), 4)))
+    g[-1, :, 1].clamp_(min=-30.0)
+    want, end = ret.gated_recurrence(x, g, form, state_out=True)
+    back = ret.gated_recurrence_backward(dh, x, g, want, form, grad_state_in=True)
+    for bad in _bad_values():
+        xb = x.clone()
+        xb[-1, N // 3, 1] = bad
+        h, s = ret.gated_recurrence(xb, g, form, state_out=True)
+        hit = torch.zeros(B, N, D, dtype=torch.bool, device=DEV)
+        hit[-1, N // 3:, 1] = True
+        assert torch.equal(~h.isfinite(), hit) and torch.equal(h[~hit], want[~hit])
+        assert (~s.isfinite()).nonzero().tolist() == [[B - 1, 1]]
+        db = dh.clone()
+        db[-1, N // 2, 1] = bad
+        for reset in (None, N // 4):
+            gr = g.clone()
+            if reset is not None:
+                gr[-1, reset, 1] = -float("inf")
+            hr = want if reset is None else ret.gated_recurrence(x, gr, form)[0]
+            ref = back if reset is None else ret.gated_recurrence_backward(dh, x, gr, hr, form, grad_state_in=True)
+            dx, dg, ds = ret.gated_recurrence_backward(db, x, gr, hr, form, grad_state_in=True)
+            hit = torch.zeros(B, N, D, dtype=torch.bool, device=DEV)
+            hit[-1, reset or 0:N // 2 + 1, 1] = True
+            assert torch.equal(dx[~hit], ref[0][~hit]) and torch.equal(dg[~hit], ref[1][~hit])
+            assert not bool(dx[hit].isfinite().any())
+            if reset is not None:
+                assert float(dg[-1, reset, 1]) == 0.0 and torch.equal(ds, ref[2])
+            else:
+                assert (~ds.isfinite()).nonzero().tolist() == [[B - 1, 1]]
+
+
+def test_a_decay_of_one_passes_over_whatever_x_holds():
+    """A gate of +inf in the sigmoid form keeps the state: padding whose x is anything, in the recurrence, its gradients
+    and its step."""
+    _announce("gates of +inf")
+    B, N, D = 2, 700, 72
+    x, dh, s0 = _randn((B, N, D), 1).to(DEV), _randn((B, N, D), 2).to(DEV), _randn((B, D), 3).to(DEV)
+    g = _gate((B, N, D), 4, F32, "sigmoid").to(DEV)
+    keep = torch.rand(B, N, 1, generator=_gen(5)).to(DEV) < 0.3
+    g = torch.where(keep, float("inf"), g)
+    want = ret.gated_recurrence(x, g, state_in=s0, state_out=True)
+    back = ret.gated_recurrence_backward(dh, x, g, want[0], state_in=s0, grad_state_in=True)
+    for bad in _bad_values():
+        xb = torch.where(keep, bad, x)
+        got = ret.gated_recurrence(xb, g, state_in=s0, state_out=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        got = ret.gated_recurrence_backward(dh, xb, g, got[0], state_in=s0, grad_state_in=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, back))
+        state = s0.clone()
+        h = ret.gated_recurrence_step(torch.full_like(s0, bad), torch.full_like(s0, float("inf")), state)
+        assert torch.equal(state, s0) and torch.equal(h, s0)
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "log"])
+def test_a_step_resets_a_slot_of_any_contents(form):
+    _announce(f"step resets {form}")
+    x = _randn((3, 70), 1).to(DEV)
+    pool = torch.stack([torch.full((70,), b) for b in _bad_values()]).to(DEV)
+    slots = torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV)
+    h = ret.gated_recurrence_step(x, torch.full_like(x, -float("inf")), pool, form, slots=slots)
+    assert torch.equal(h, x) and torch.equal(pool[slots.long()], x)
+    pool = torch.full((1, 70), float("inf"), device=DEV)
+    for _ in range(3):
+        h = ret.gated_recurrence_step(x[:1], torch.full_like(x[:1], -1e-3 if form == "log" else 5.0), pool, form)
+        assert not bool(h.isfinite().any())
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "log"])
+def test_a_reset_ends_a_gate_of_nan(form):
+    _announce(f"gate of nan {form}")
+    B, N, D = 2, 1500, 40
+    x, s0 = _randn((B, N, D), 1).to(DEV), _randn((B, D), 2).to(DEV)
+    g = _mixed((B, N, D), form, 3).to(DEV)
+    for at, reset in ((0, 1), (100, 103), (100, 900), (0, N - 1)):
+        gr = g.clone()
+        gr[1, reset, 7] = -float("inf")
+        want = ret.gated_recurrence(x, gr, form, state_in=s0, state_out=True)
+        gr[1, at, 7] = float("nan")
+        h, s = ret.gated_recurrence(x, gr, form, state_in=s0, state_out=True)
+        hit = torch.zeros(B, N, D, dtype=torch.bool, device=DEV)
+        hit[1, at:reset, 7] = True
+        assert torch.equal(h.isnan(), hit) and torch.equal(h[~hit], want[0][~hit]) and torch.equal(s, want[1])
