@@ -1076,3 +1076,130 @@ def test_a_reset_ends_a_gate_of_nan(form):
         hit = torch.zeros(B, N, D, dtype=torch.bool, device=DEV)
         hit[1, at:reset, 7] = True
         assert torch.equal(h.isnan(), hit) and torch.equal(h[~hit], want[0][~hit]) and torch.equal(s, want[1])
+
+
+# ---------------------------------------------------------------------------
+# Norms whose workgroups take several turns
+
+
+def _turns(rows, at_once, parts):
+    return -(-rows // (at_once * parts))
+
+
+def _head_plan(H, rows, d, dtype):
+    """(turns of the forward, turns of the backward) of the gated norm, by the launches' rules."""
+    V = 4 if dtype == F32 else 8
+    at_once = 256 // (8 if d <= 8 * V else 16 if d <= 16 * V else 32 if d <= 32 * V else 64)
+    want = -(-rows // at_once)
+    back = max(512, min(4096, H * want // 8))
+    return (_turns(rows, at_once, min(want, -(-4096 // H))), _turns(rows, at_once, min(want, -(-back // H))))
+
+
+def _row_plan(rows, D):
+    """The same of the residual norm."""
+    at_once = 4 if D <= 1024 else 1
+    want = -(-rows // at_once)
+    back = 1024 if D <= 2048 else 512 if D <= 4096 else 256
+    return _turns(rows, at_once, min(want, 4096)), _turns(rows, at_once, min(want, back))
+
+
+@pytest.mark.parametrize("rms, gated, which", [(False, True, "wb"), (True, False, "w")])
+@pytest.mark.parametrize("d, dtype", [(64, BF16), (33, BF16), (5, BF16), (128, BF16), (97, BF16), (256, BF16), (200, BF16), (512, BF16),
+                                      (505, BF16), (1024, BF16), (1000, BF16), (32, F32), (61, F32), (128, F32), (97, F32), (256, F32),
+                                      (512, F32), (1024, F32), (1001, F32)])
+def test_gated_norm_backward_over_several_turns(d, dtype, rms, gated, which):
+    """Two workgroups a head, four turns each, the last one partly past the rows; the batch's rows end inside a turn."""
+    V = 4 if dtype == F32 else 8
+    at_once = 256 // (8 if d <= 8 * V else 16 if d <= 16 * V else 32 if d <= 32 * V else 64)
+    B, H, N = 2, 256, (7 * at_once - 2) // 2
+    _announce(f"gated norm backward, turns {B, H, N, d} {dtype} rms={rms}")
+    assert _head_plan(H, B * N, d, dtype)[1] >= 3 and N % (2 * at_once) and B * N % at_once
+    shape = (B, H, N, d)
+    o, dy = _randn(shape, 1, dtype, 2.0, 0.5), _randn(shape, 2, dtype)
+    gate = _randn(shape, 3, dtype, 3.0) if gated else None
+    w, b, params = _norm_params(H * d, 4, which)
+    got = ret.gated_norm_backward(dy.to(DEV), o.to(DEV), None if gate is None else gate.to(DEV), ret.Norm(EPS, rms=rms, **params))
+    args = (o, gate, w, b, EPS, rms)
+    refs, errs = orc.gated_norm_backward(dy, *args), orc.gated_norm_backward_error(dy, *args)
+    for t, ref, e, what in zip(got, refs, errs, ("grad_o", "grad_gate", "grad_weight", "grad_bias")):
+        if t is not None:
+            _check(t, ref, e, what)
+
+
+@pytest.mark.parametrize("d, dtype", [(64, BF16), (33, BF16), (5, BF16), (128, BF16), (97, BF16), (256, BF16), (200, BF16), (512, BF16),
+                                      (505, BF16), (1024, BF16), (1000, BF16), (32, F32), (61, F32), (128, F32), (97, F32), (256, F32),
+                                      (512, F32), (1024, F32), (1001, F32)])
+def test_gated_norm_over_several_turns(d, dtype):
+    """256 heads, 16 workgroups each, four turns; some heads (rows do not meet) against the oracle."""
+    V = 4 if dtype == F32 else 8
+    at_once = 256 // (8 if d <= 8 * V else 16 if d <= 16 * V else 32 if d <= 32 * V else 64)
+    B, H, N = 3, 256, 17 * at_once - 1
+    _announce(f"gated norm, turns {B, H, N, d} {dtype}")
+    assert _head_plan(H, B * N, d, dtype)[0] >= 4 and N % (16 * at_once) and B * N % at_once
+    shape, heads = (B, H, N, d), [0, 1, 130, 255]
+    gen = torch.Generator(DEV).manual_seed(d)
+    o = (2 * torch.randn(shape, generator=gen, device=DEV) + 0.5).to(dtype)
+    gate = (3 * torch.randn(shape, generator=gen, device=DEV)).to(dtype)
+    w, b, params = _norm_params(H * d, 4, "wb")
+    y = ret.gated_norm(o, gate, ret.Norm(EPS, **params))
+    at = lambda p: p.view(H, d)[heads].reshape(-1)  # noqa: E731
+    args = (o[:, heads].cpu(), gate[:, heads].cpu(), at(w), at(b), EPS, False)
+    _check(y[:, heads], orc.gated_norm(*args), orc.gated_norm_error(*args), "y")
+    assert not bool(y.isnan().any())
+
+
+@pytest.mark.parametrize("B, N, D, dtype, stream", [
+    (3, 4111, 7, BF16, F32), (2, 6163, 64, BF16, BF16), (3, 4111, 128, BF16, F32), (5, 2467, 97, F32, F32), (2, 6163, 500, BF16, BF16),
+    (3, 4111, 512, BF16, F32), (2, 6163, 1000, BF16, BF16), (3, 1033, 1100, BF16, F32), (2, 1549, 2048, BF16, BF16), (3, 1033, 2048, F32, F32),
+    (3, 517, 2100, BF16, BF16), (3, 517, 4096, BF16, F32), (5, 311, 4095, F32, F32)])
+@pytest.mark.parametrize("rms, scaled, residual", [(False, True, False), (True, False, True)])
+def test_residual_norm_backward_over_several_turns(B, N, D, dtype, stream, rms, scaled, residual):
+    """Four turns a workgroup, the last one partly past the rows, and batches whose rows end inside a turn."""
+    _announce(f"residual norm backward, turns {B, N, D} {dtype} {stream} rms={rms}")
+    assert _row_plan(B * N, D)[1] >= 4
+    shape = (B, N, D)
+    x, res = _randn(shape, 1, dtype), _randn(shape, 2, stream, 2.0, 0.5)
+    dy, dr = _randn(shape, 3, dtype), _randn(shape, 4, stream)
+    scale = _randn((D,), 5, F32, 0.2, 0.7) if scaled else None
+    w, b, params = _norm_params(D, 6, "wb")
+    norm, alpha = ret.Norm(EPS, rms=rms, **params), 1.75 if scaled else 1.0
+    sd = None if scale is None else scale.to(DEV)
+    _, r = ret.residual_norm(x.to(DEV), res.to(DEV), norm, scale=sd, alpha=alpha)
+    got = ret.residual_norm_backward(dy.to(DEV), None if residual else r, norm, grad_r=dr.to(DEV), x=x.to(DEV), scale=sd, alpha=alpha,
+                                     residual=res.to(DEV) if residual else None)
+    row = orc.residual_norm(x, res, w, b, EPS, rms, scale, alpha)[1] if residual else r.cpu()
+    args = (dy, dr, row, w, EPS, rms, x, scale, alpha)
+    refs, errs = orc.residual_norm_backward(*args), orc.residual_norm_backward_error(*args)
+    grow = 1.0
+    if residual:  # the row formed again: 4 steps of its terms, as in test_residual_norm_matches_the_oracle
+        terms = np.abs(alpha * orc.f64(res)) + np.abs(orc.f64(x) * (1.0 if scale is None else orc.f64(scale)))
+        grow = 1 + float((terms.max(-1) / np.abs(row).max(-1)).max())
+    for t, ref, e, what in zip(got, refs, errs, ("grad_x", "grad_residual", "grad_scale", "grad_weight", "grad_bias")):
+        if t is not None:
+            _check(t, ref, grow * e, what)
+
+
+@pytest.mark.parametrize("B, N, D, dtype, stream", [
+    (3, 16411, 7, BF16, F32), (2, 24593, 64, BF16, BF16), (3, 16411, 97, F32, F32), (3, 16411, 500, BF16, F32), (2, 24593, 1000, BF16, BF16),
+    (3, 4111, 1100, BF16, F32), (2, 6163, 2048, BF16, BF16), (3, 4111, 2100, F32, F32), (2, 6163, 4096, BF16, F32), (3, 4111, 5000, BF16, BF16)])
+def test_residual_norm_over_several_turns(B, N, D, dtype, stream):
+    """Four turns a workgroup: rows of every turn against the oracle, the rest against the same rows on their own."""
+    _announce(f"residual norm, turns {B, N, D} {dtype} {stream}")
+    assert _row_plan(B * N, D)[0] >= 4
+    gen = torch.Generator(DEV).manual_seed(D)
+    x = torch.randn((B, N, D), generator=gen, device=DEV).to(dtype)
+    res = (2 * torch.randn((B, N, D), generator=gen, device=DEV) + 0.5).to(stream)
+    w, b, params = _norm_params(D, 6, "wb")
+    scale = _randn((D,), 5, F32, 0.2, 0.7)
+    norm = ret.Norm(EPS, **params)
+    y, r = ret.residual_norm(x, res, norm, scale=scale.to(DEV), alpha=1.75)
+    rows = sorted({*range(0, B * N, 997), N - 1, N, B * N - 2, B * N - 1})
+    args = (x.view(-1, D)[rows].cpu(), res.view(-1, D)[rows].cpu(), w, b, EPS, False, scale, 1.75)
+    refs, errs = orc.residual_norm(*args), orc.residual_norm_error(*args)
+    _check(y.view(-1, D)[rows], refs[0], errs[0], "y")
+    _check(r.view(-1, D)[rows], refs[1], errs[1], "r")
+    step = 4000  # at most one turn
+    for at in range(0, B * N, step):
+        some = slice(at, at + step)
+        y1, r1 = ret.residual_norm(x.view(-1, D)[some], res.view(-1, D)[some], norm, scale=scale.to(DEV), alpha=1.75)
+        assert torch.equal(y.view(-1, D)[some], y1) and torch.equal(r.view(-1, D)[some], r1)
