@@ -15,7 +15,9 @@
  *     must not have two elements in one place. The stride of a dimension of
  *     size 1 is not read.
  *   - An output must not share bytes with an input or another output; the
- *     whole range a view spans counts. Such calls are refused with
+ *     whole range a view spans counts, unless the two are columns of one larger
+ *     tensor side by side (rows, or tokens of heads that follow one another, at
+ *     the same distance). Such calls are refused with
  *     RET_ERR_INVALID_ARG, as are null pointers where a tensor is required,
  *     sizes <= 0 and misaligned data; RET_ERR_UNSUPPORTED: sizes beyond the
  *     limits stated at each function.

@@ -94,33 +94,38 @@ int check_view(const retention_view_t* v, int B, int H, int N, int d, int dtype,
     if (stride[i] > kMaxSpan / size[i]) return RET_ERR_UNSUPPORTED;
     last += (size[i] - 1) * stride[i];
   }
-  if (is_output) {
-    // From the smallest stride up, each must step over all that the smaller ones span.
-    int order[3] = {0, 1, 2};
-    for (int i = 0; i < 2; ++i)
-      for (int j = 0; j < 2 - i; ++j)
-        if (stride[order[j]] > stride[order[j + 1]]) {
-          const int t = order[j];
-          order[j] = order[j + 1];
-          order[j + 1] = t;
-        }
+  // Dimensions from the smallest stride up.
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[order[j]] > stride[order[j + 1]]) {
+        const int t = order[j];
+        order[j] = order[j + 1];
+        order[j + 1] = t;
+      }
+  if (is_output) {  // each stride must step over all that the smaller ones span
     int64_t span = d;
-    for (int i = 0; i < 3; ++i) {
-      if (size[order[i]] == 1) continue;
-      if (stride[order[i]] < span) return RET_ERR_INVALID_ARG;
-      span += (size[order[i]] - 1) * stride[order[i]];
+    for (int i : order) {
+      if (size[i] == 1) continue;
+      if (stride[i] < span) return RET_ERR_INVALID_ARG;
+      span += (size[i] - 1) * stride[i];
     }
   }
   *out = View{static_cast<char*>(v->data), stride[0], stride[1], stride[2]};
   *range = range_of(v->data, (last + d) * es);
-  int64_t pitch = 0;  // the smallest stride, if it divides the others and holds a row
-  for (int i = 0; i < 3; ++i)
-    if (size[i] > 1 && (pitch == 0 || stride[i] < pitch)) pitch = stride[i];
-  for (int i = 0; i < 3; ++i)
-    if (pitch != 0 && stride[i] % pitch != 0) pitch = 0;
-  if (pitch >= d) {
+  // Dimensions that go on where the smaller ones end (heads of a token) widen
+  // the columns; the pitch is the next stride, if it divides the others and
+  // holds the columns.
+  int64_t width = d, pitch = 0;
+  for (int i : order) {
+    if (stride[i] == 0) continue;  // adds no place
+    if (pitch == 0 && stride[i] == width) width *= size[i];
+    else if (pitch == 0) pitch = stride[i];
+    else if (stride[i] % pitch != 0) return RET_OK;
+  }
+  if (pitch >= width) {
     range->pitch = static_cast<uintptr_t>(pitch * es);
-    range->width = static_cast<uintptr_t>(static_cast<int64_t>(d) * es);
+    range->width = static_cast<uintptr_t>(width * es);
   }
   return RET_OK;
 }

@@ -411,3 +411,23 @@ def test_the_dtype_of_h():
     for bad, dtype in ((torch.zeros(1, dtype=bf16), f32), (torch.float64, f32), (torch.float16, bf16)):
         with pytest.raises(ValueError, match="out must be"):
             block._h_dtype(bad, "out", dtype)
+
+
+@shim_only
+def test_heads_of_one_tensor_may_lie_side_by_side(lib):
+    """x, gate and h as thirds of one [B, N, 3, H, d] tensor, 3 elements to a row more or none; a shift by one element, or
+    heads of all three in turn ([B, N, H, 3, d], where h's d lie between the others'), told by their places."""
+    B, H, N, d = 2, 5, 10, 24
+    for more in (0, 3):
+        pitch = 3 * H * d + more
+
+        def call(shift=0, head_stride=d, third=H * d):
+            st = (N * pitch, head_stride, pitch)
+            v = [_v(A[0] + 2 * (third * i + (shift if i == 2 else 0)), *st) for i in range(3)]
+            return lib.retention_gated_recurrence(*v, B, H, N, d, 0, 1, None, None, None, B, N, WS, 1 << 40, None)
+
+        assert call() == 0
+        assert call(shift=-1) == INVALID and call(third=H * d - 8) == INVALID
+        assert call(shift=1) == (INVALID if more == 0 else 0)  # into the row's spare elements
+        # One head's thirds beside one another: columns of d at a distance of 3 d, if that divides the rows' distance.
+        assert call(head_stride=3 * d, third=d) == (0 if more == 0 else INVALID)

@@ -1203,3 +1203,70 @@ def test_residual_norm_over_several_turns(B, N, D, dtype, stream):
         some = slice(at, at + step)
         y1, r1 = ret.residual_norm(x.view(-1, D)[some], res.view(-1, D)[some], norm, scale=scale.to(DEV), alpha=1.75)
         assert torch.equal(y.view(-1, D)[some], y1) and torch.equal(r.view(-1, D)[some], r1)
+
+
+# ---------------------------------------------------------------------------
+# Layouts together
+
+
+@pytest.mark.parametrize("dtype, form", [(BF16, "sigmoid"), (F32, "log"), (BF16, "log"), (F32, "sigmoid")])
+@pytest.mark.parametrize("d, heads", [(72, 0), (33, 0), (24, 3), (7, 5), (200, 2)])
+def test_packed_sequences_in_any_layout(d, heads, dtype, form):
+    """Ragged sequences in slices of a fused projection, in token-major heads and in gradients side by side: to the bit
+    those of contiguous tensors, and nothing beside them is written."""
+    _announce(f"packed layouts {d} {heads} {dtype} {form}")
+    lens = [300, 0, 1, 700, 65, 0, 2, 129]
+    cu = torch.tensor(np.concatenate([[2], 2 + np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+    T, S = int(cu[-1]) + 5, len(lens)
+    lead, states = ((1, heads), (S, heads, d)) if heads else ((1,), (S, d))
+    shape = (*lead, T, d)
+    x, g, dh = (t.to(DEV) for t in (_randn(shape, 1, dtype), _gate(shape, 2, dtype, form), _randn(shape, 3, dtype)))
+    s0, ds = _randn(states, 4).to(DEV), _randn(states, 5).to(DEV)
+    zeros = lambda: torch.zeros(shape, dtype=dtype, device=DEV)  # noqa: E731
+    want = ret.gated_recurrence(x, g, form, state_in=s0, state_out=True, cu_seqlens=cu, out=zeros())
+    back = ret.gated_recurrence_backward(dh, x, g, want[0], form, state_in=s0, grad_state_out=ds, grad_state_in=True, cu_seqlens=cu,
+                                         grads=(zeros(), zeros()))
+
+    def fused(n):  # n tensors of this shape as columns of one [1, T, ...], heads token-major
+        width = max(heads, 1) * d
+        both = torch.full((1, T, n * width + 3), 5.0, dtype=dtype, device=DEV)
+        cut = [both[..., 3 + i * width: 3 + (i + 1) * width] for i in range(n)]
+        return both, [c.unflatten(-1, (heads, d)).transpose(1, 2) if heads else c for c in cut]
+
+    _, (xf, gf, hf, dhf) = fused(4)
+    for to, t in ((xf, x), (gf, g), (dhf, dh)):
+        to.copy_(t)
+    hf.zero_()
+    _, s1 = ret.gated_recurrence(xf, gf, form, state_in=s0, state_out=True, cu_seqlens=cu, out=hf)
+    assert torch.equal(hf, want[0]) and torch.equal(s1, want[1])
+    whole, (dxf, dgf) = fused(2)
+    dxf.zero_(), dgf.zero_()
+    got = ret.gated_recurrence_backward(dhf, xf, gf, hf, form, state_in=s0, grad_state_out=ds, grad_state_in=True, cu_seqlens=cu,
+                                        grads=(dxf, dgf))
+    assert all(torch.equal(a, b) for a, b in zip(got, back))
+    assert bool((whole[..., :3] == 5).all()) and bool((hf[..., :2, :] == 0).all()) and bool((dxf[..., T - 5:, :] == 0).all())
+
+
+@pytest.mark.parametrize("shape, pitch, form, dtype", [
+    ((1, 17600, 1001), 1001, "sigmoid", F32), ((3, 12000, 1003), 1010, "log", BF16), ((300, 130, 1000), 1004, "sigmoid", BF16),
+    ((1, 17600, 1000), 1024, "log", F32), ((2, 12000, 2000), 2048, "sigmoid", BF16)])
+def test_wide_gradients_in_rows_that_begin_anywhere(shape, pitch, form, dtype):
+    """Gradients too large for the caches, in rows on cache lines and off them: some channels of a few rows against the
+    oracle, and nothing written beside the rows."""
+    _announce(f"wide gradients {shape} pitch {pitch} {form} {dtype}")
+    B, N, D = shape
+    at = [*range(10), *range(60, 70), *range(D - 70, D - 60), *range(D - 9, D)]
+    x, g, dh, s0, ds = _randn(shape, 1, dtype), _gate(shape, 2, dtype, form), _randn(shape, 3, dtype), _randn((B, D), 4), _randn((B, D), 5)
+    rows = [0, B - 1]
+    some = [t[rows][..., at] for t in (dh, x, g)]
+    s0s, dss = s0[rows][..., at], ds[rows][..., at]
+    dev = [t.to(DEV) for t in (dh, x, g, s0, ds)]
+    h = ret.gated_recurrence(dev[1], dev[2], form, state_in=dev[3])[0]
+    wide = torch.full((2, B, N, pitch), float("nan"), dtype=dtype, device=DEV)
+    dx, dg, ds0 = ret.gated_recurrence_backward(*dev[:3], h, form, state_in=dev[3], grad_state_out=dev[4], grad_state_in=True,
+                                                grads=(wide[0, ..., :D], wide[1, ..., :D]))
+    args = (*some, h[rows][..., at].cpu(), form, s0s, dss)
+    refs, errs = orc.recurrence_backward(*args), orc.recurrence_backward_error(*args)
+    for got, ref, e, what in zip((dx, dg, ds0), refs, errs, ("grad_x", "grad_gate", "grad_state_in")):
+        _check(got[rows][..., at], ref, e, what)
+    assert bool(torch.isnan(wide[..., D:]).all()) and not bool(torch.isnan(wide[..., :D]).any())
