@@ -90,7 +90,12 @@ enum retention_gate_form {
  * workspace: retention_gated_recurrence_workspace_bytes(...) bytes (packed:
  * whether there are cu_seqlens; the same for the backward), 8-byte aligned; its
  * contents on entry do not matter. Calls that may overlap in time need one
- * each.
+ * each: parts of a long sequence wait there for one another. Such a wait ends
+ * after a million looks (about a second) whatever happens; the results behind
+ * it are then NaN. The first four bytes of the workspace (where the call needs
+ * one) say afterwards which it was: all ones where every wait was met, 0 where
+ * one was given up, which takes a workspace that something else wrote to
+ * during the call, or a GPU that stood still.
  */
 size_t retention_gated_recurrence_workspace_bytes(int sequences, int H, int N, int max_len, int packed, int d,
                                                   int dtype);

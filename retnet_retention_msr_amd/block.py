@@ -254,6 +254,11 @@ def gated_recurrence(x, gate, form: str = "sigmoid", state_in=None, state_out: U
     [S, ...] and ``max_len`` (default N) bounds a sequence's length. Tokens
     outside every sequence, or beyond max_len of one, are not written, so in
     an output allocated here they are undefined.
+
+    ``workspace``: at least gated_recurrence_workspace_bytes, of this call alone
+    while it runs. If its first four bytes (where any are needed) are 0
+    afterwards, a wait between parts of a sequence was given up after about a
+    second and the results behind it are NaN; they are all ones otherwise.
     """
     dt = _activations(x, "x", (3, 4))
     like = _Like(x)

@@ -27,8 +27,8 @@ struct Sequences {
 // Planning of a recurrence call: a pure function of the sizes. A unit is a
 // sequence's (or head's) slab of kScanChannels channels; it is cut into tiles
 // of `rows` tokens, one workgroup of `waves` waves of `wave_rows` tokens each.
-// With more than one tile the workspace holds, per unit, a ticket and, per
-// tile and channel, what the tile passes on (recurrence.hip). Lanes take `vec`
+// With more than one tile the workspace holds a status word and, per unit, a
+// ticket and, per tile and channel, what the tile passes on (recurrence.hip). Lanes take `vec`
 // channels, or one where the whole row is shorter: four of them, 16 bytes of
 // fp32 and 8 of bf16, and in bf16's backward eight. A lane then holds fewer
 // tokens, and more lanes' folds have to be joined (24 exchanges of three words
@@ -39,6 +39,7 @@ struct Sequences {
 constexpr int kScanChannels = 64;
 constexpr uint32_t kXcds = 8, kXcdUnits = 9;
 constexpr int kScanMaxWaves = 8;
+constexpr size_t kScanStatusBytes = 256;  // of the workspace: the status word, then nothing
 // Tokens of a wave: forward 32 against 16, 320 us against 442 at 8 x 8192 x
 // 4096. The sigmoid form's backward reads four tensors; waves of 16 tokens let
 // it hold them in 128 registers, four waves to a SIMD: 605 us against 705 with
@@ -110,7 +111,7 @@ inline ScanPlan plan_scan(int S, int H, int N, int max_len, bool packed, int d, 
   p.blocks = int64_t{scan_round(static_cast<uint32_t>(together))} * (columns * p.slots / together);
   p.folds = packed || p.units < kScanManyUnits;
   if (p.tiles > 1)
-    p.bytes = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
+    p.bytes = kScanStatusBytes + (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256 +
               static_cast<size_t>(columns) * p.slots * kScanChannels * (p.folds ? 12 : 4);
   return p;
 }

@@ -141,6 +141,7 @@ __device__ __forceinline__ bool wave_special(const float (&A)[V], const float (&
 // the tiles of its sequences have the slots s * tiles + tile, or, packed,
 // floor(first token / rows) + s + tile, which no two of them share.
 struct ScanWords {
+  uint32_t* status;  // 0 where a wait was given up
   uint32_t* ticket;  // [units], from all ones up
   uint32_t* state;   // [columns][slots][64]: the state after the tile
   uint64_t* fold;    // [columns][slots][64]: Y, decay_word(A, M); null: states alone
@@ -184,8 +185,8 @@ __device__ __forceinline__ float fold_on(float m, float Y, float y) {
 // many units the nearest state is mostly there, and reading further tiles'
 // words for it costs 2%; four at a time cost registers: 4% of the log backward). `fold`
 // and `state` are the words of the unit's tile 0, 64 words a tile. Polls at
-// most kPolls times (about a second), then gives NaN: a wave reaches the end
-// whatever the workspace holds.
+// most kPolls times (about a second), then gives NaN and says so in the status
+// word: a wave reaches the end whatever the workspace holds.
 constexpr int kAhead = 2;
 constexpr int kDepth = 32;
 constexpr int kPolls = 1 << 20;
@@ -231,28 +232,31 @@ __device__ __forceinline__ bool look(const uint64_t* fold, const uint32_t* state
   return false;
 }
 
-__device__ __forceinline__ float look_back(const uint64_t* fold, const uint32_t* state, int tile, Stash& stash,
-                                           int lane) {
+__device__ __forceinline__ float give_up(uint32_t* status) {
+  __hip_atomic_store(status, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __uint_as_float(0x7fc00000u);
+}
+__device__ __forceinline__ float look_back(uint32_t* status, const uint64_t* fold, const uint32_t* state, int tile,
+                                           Stash& stash, int lane) {
   int depth = 0;
-  float y = __uint_as_float(0x7fc00000u);
+  float y;
   for (int poll = 0; poll < kPolls; ++poll) {
     if (depth == 0 ? look<1>(fold, state, tile, stash, lane, depth, y)
                    : look<kAhead>(fold, state, tile, stash, lane, depth, y))
-      break;
+      return y;
   }
-  return y;
+  return give_up(status);
 }
 
 // The same from the last tile's state alone.
-__device__ __forceinline__ float last_state(const uint32_t* state, int tile) {
-  uint32_t s = ~0u;
+__device__ __forceinline__ float last_state(uint32_t* status, const uint32_t* state, int tile) {
   for (int poll = 0; poll < kPolls; ++poll) {
-    s = __hip_atomic_load(state + static_cast<int64_t>(tile - 1) * kScanChannels, __ATOMIC_RELAXED,
-                          __HIP_MEMORY_SCOPE_AGENT);
-    if (__all(s != ~0u)) break;
+    const uint32_t s = __hip_atomic_load(state + static_cast<int64_t>(tile - 1) * kScanChannels, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    if (__all(s != ~0u)) return __uint_as_float(s);
     __builtin_amdgcn_s_sleep(1);
   }
-  return __uint_as_float(s);  // all ones, a NaN, where it never came
+  return give_up(status);
 }
 
 // What a workgroup shares. Channel i of the slab is fold[wave][kPad + i]; the
@@ -458,9 +462,9 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
     } else {
       if (w.fold) {
         if (!end) publish(w.fold + here, m, TY);
-        carry = look_back(w.fold + word, w.state + word, p.tile, shared.stash, lane);
+        carry = look_back(w.status, w.fold + word, w.state + word, p.tile, shared.stash, lane);
       } else {
-        carry = last_state(w.state + word, p.tile);
+        carry = last_state(w.status, w.state + word, p.tile);
       }
     }
     const float after = fold_on(m, TY, carry);
@@ -909,6 +913,8 @@ hipError_t scan_words(const ScanPlan& p, void* workspace, ScanWords* words, hipS
   *words = ScanWords{};
   if (p.tiles <= 1) return hipSuccess;
   char* base = static_cast<char*>(workspace);
+  words->status = reinterpret_cast<uint32_t*>(base);
+  base += kScanStatusBytes;
   words->ticket = reinterpret_cast<uint32_t*>(base);
   base += (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256;
   words->state = reinterpret_cast<uint32_t*>(base);

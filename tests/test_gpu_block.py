@@ -1270,3 +1270,18 @@ def test_wide_gradients_in_rows_that_begin_anywhere(shape, pitch, form, dtype):
     for got, ref, e, what in zip((dx, dg, ds0), refs, errs, ("grad_x", "grad_gate", "grad_state_in")):
         _check(got[rows][..., at], ref, e, what)
     assert bool(torch.isnan(wide[..., D:]).all()) and not bool(torch.isnan(wide[..., :D]).any())
+
+
+@pytest.mark.parametrize("shape, cu", [((1, 20000, 64), None), ((260, 300, 64), None), ((1, 4000, 40), [0, 3000, 3000, 3999])])
+def test_the_status_word_says_that_every_wait_was_met(shape, cu):
+    _announce(f"status word {shape}")
+    x, g = _randn(shape, 1).to(DEV), _gate(shape, 2, F32, "log").to(DEV)
+    cu = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    S = shape[0] if cu is None else cu.numel() - 1
+    n = ret.gated_recurrence_workspace_bytes(S, 1, shape[1], shape[2], F32, max_len=None if cu is None else shape[1])
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    h, _ = ret.gated_recurrence(x, g, "log", workspace=ws, cu_seqlens=cu)
+    assert ws[:4].tolist() == [255] * 4
+    ws.zero_()
+    ret.gated_recurrence_backward(x, None, g, h, "log", workspace=ws, cu_seqlens=cu)
+    assert ws[:4].tolist() == [255] * 4
