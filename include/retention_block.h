@@ -183,7 +183,9 @@ int retention_gated_norm_backward(const retention_view_t* grad_y, const retentio
  * over rows of D <= RETENTION_MAX_MODEL_DIM values. x and y are [B, 1, N, D]
  * of type dtype; residual and r have type stream_dtype, dtype or RET_F32.
  * scale (device fp32 [D], NULL: 1) weighs the branch per channel, alpha
- * (finite) the residual. y is formed from r before its rounding.
+ * (finite) the residual. y is formed from r before its rounding. r may be the
+ * residual itself (the same data and strides): the stream is then updated in
+ * place.
  */
 int retention_residual_norm(const retention_view_t* x, const retention_view_t* residual, const retention_view_t* y,
                             const retention_view_t* r, int B, int N, int D, int dtype, int stream_dtype,

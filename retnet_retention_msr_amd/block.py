@@ -449,7 +449,7 @@ def residual_norm(x, residual, norm: NormLike, scale=None, alpha: float = 1.0, o
 
     x and residual are [..., D]; the residual stream (residual and r) has x's
     dtype or float32, y has x's. ``scale`` (fp32 [D], default 1) weighs the
-    branch per channel.
+    branch per channel. ``residual_out`` may be ``residual`` itself.
     """
     dt, like = _activations(x, "x", _ROWS), _rows_like(x)
     dims, dev = _row_dims(like.shape), like.device

@@ -376,15 +376,17 @@ int retention_residual_norm(const retention_view_t* x, const retention_view_t* r
   NormArgs n;
   if ((st = check_norm(norm, D, &n, &ranges)) != RET_OK) return st;
   View vx, vres, vy, vr;
-  Range g;
+  Range g, res;
   if ((st = check_view(x, B, 1, N, D, dtype, true, false, &vx, &g)) != RET_OK) return st;
   ranges.input(g);
-  if ((st = check_view(residual, B, 1, N, D, stream_dtype, true, false, &vres, &g)) != RET_OK) return st;
-  ranges.input(g);
+  if ((st = check_view(residual, B, 1, N, D, stream_dtype, true, false, &vres, &res)) != RET_OK) return st;
   if ((st = check_view(y, B, 1, N, D, dtype, true, true, &vy, &g)) != RET_OK) return st;
   ranges.output(g);
   if ((st = check_view(r, B, 1, N, D, stream_dtype, true, true, &vr, &g)) != RET_OK) return st;
   ranges.output(g);
+  // r may be the residual itself: a thread reads its values of a row before it
+  // writes them, and no other takes them for its own.
+  if (vr.data != vres.data || vr.sb != vres.sb || vr.sn != vres.sn) ranges.input(res);
   if ((st = check_float_array(scale, D, &g)) != RET_OK) return st;
   ranges.input(g);
   if (ranges.clash()) return RET_ERR_INVALID_ARG;

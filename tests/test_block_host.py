@@ -431,3 +431,16 @@ def test_heads_of_one_tensor_may_lie_side_by_side(lib):
         assert call(shift=1) == (INVALID if more == 0 else 0)  # into the row's spare elements
         # One head's thirds beside one another: columns of d at a distance of 3 d, if that divides the rows' distance.
         assert call(head_stride=3 * d, third=d) == (0 if more == 0 else INVALID)
+
+
+def test_the_residual_stream_may_be_updated_in_place(lib):
+    """r is the residual itself or lies apart from it; shifted, or with other strides, it is refused, as is y in its place."""
+    st = (10 * 64, 0, 64)
+
+    def call(r, strides=st, y=A[2]):
+        return lib.retention_residual_norm(_v(A[0], *st), _v(A[1], *st), _v(y, *st), _v(r, *strides), 2, 10, 64, 1, 1, _norm(), None,
+                                           1.0, None)
+
+    assert call(A[1] + 2) == call(A[1] + 128) == call(A[1], (64, 0, 128)) == call(A[1], y=A[1]) == call(A[0]) == INVALID
+    if SHIM:
+        assert call(A[1]) == call(A[3]) == 0

@@ -1285,3 +1285,22 @@ def test_the_status_word_says_that_every_wait_was_met(shape, cu):
     ws.zero_()
     ret.gated_recurrence_backward(x, None, g, h, "log", workspace=ws, cu_seqlens=cu)
     assert ws[:4].tolist() == [255] * 4
+
+
+@pytest.mark.parametrize("shape, dtype, stream", [((1, 1), BF16, BF16), ((3, 65), BF16, F32), ((8, 4096), BF16, BF16), ((700, 1001), F32, F32),
+                                                  ((5, 9001), BF16, F32), ((2, 9000, 1100), BF16, BF16), ((3, 17000, 97), BF16, F32),
+                                                  ((4, 16383), BF16, BF16), ((4, 16384), F32, F32)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_the_residual_stream_in_place(shape, dtype, stream, strided):
+    """residual_out=residual gives what a tensor of its own gives, to the bit, odd widths (threads that read beside their
+    own channels) and several turns a workgroup included."""
+    _announce(f"residual in place {shape} {dtype} {stream} strided={strided}")
+    gen = torch.Generator(DEV).manual_seed(len(shape))
+    x = torch.randn(shape, generator=gen, device=DEV).to(dtype)
+    res = torch.randn(shape, generator=gen, device=DEV).to(stream)
+    norm = ret.Norm(EPS, _randn((shape[-1],), 1).to(DEV), rms=True)
+    scale = _randn((shape[-1],), 2).to(DEV)
+    want = ret.residual_norm(x, res, norm, scale=scale, alpha=1.25)
+    place = _strided(res, 0) if strided else res.clone()
+    y, r = ret.residual_norm(x, place, norm, scale=scale, alpha=1.25, residual_out=place)
+    assert r is place and torch.equal(y, want[0]) and torch.equal(place, want[1])
