@@ -40,11 +40,12 @@ constexpr int kScanChannels = 64;
 constexpr uint32_t kXcds = 8, kXcdUnits = 9;
 constexpr int kScanMaxWaves = 8;
 constexpr size_t kScanStatusBytes = 256;  // of the workspace: the status word, then nothing
-// Tokens of a wave: forward 32 against 16, 320 us against 442 at 8 x 8192 x
-// 4096. The sigmoid form's backward reads four tensors; waves of 16 tokens let
-// it hold them in 128 registers, four waves to a SIMD: 605 us against 705 with
-// 32 at the same size. 8 where a lane has one channel, so that a short row's
-// tile stays in registers.
+// Tokens of a wave: forward 32 against 16, bf16, 302 us against 320 at 8 x 8192 x
+// 4096, 157 against 187 at 4 x 8192 x 4096 in the log form. The sigmoid form's
+// backward reads four tensors; waves of 16 tokens let it hold them in 128
+// registers, four waves to a SIMD: 622 us at 8 x 8192 x 4096 against 987 with
+// 32, of which 49 registers spill. 8 where a lane has one channel, so that a
+// short row's tile stays in registers.
 constexpr int kScanRows = 32;
 constexpr int kScanSigmoidBackRows = 16;
 constexpr int kScanNarrowRows = 8;
@@ -64,16 +65,16 @@ struct ScanPlan {
 // and wait for none of the others, and the smaller workgroups keep loads and
 // stores of different ones side by side; with few, the tiles of a unit wait
 // for one another, and half as many of them, twice as long, wait less. Forward,
-// bf16, us at four and at eight: 512 units (8 x 8192 x 4096) 307 and 335, 256
-// units (4 x 8192 x 4096) 153 and 152, 32 units (65536 x 2048) 186 and 174, 4
-// units (32768 x 256) 29 and 21. Backward, log form: 240 units (15 x 4096 x
-// 1024) 130 and 132, 128 units 78 and 78, 32 units (65536 x 2048) 299 and 286,
-// 16 units (8192 x 1024) 31 and 25. The tiles of a sequence are
-// equally long: 130 tokens as two of three waves, not of four and one, 90 us
-// against 113 at 240 x 130 x 2048.
+// bf16, us at four and at eight: 512 units (8 x 8192 x 4096) 302 and 338, 256
+// units (4 x 8192 x 4096) 154 and 148, 32 units (65536 x 2048) 194 and 184, 4
+// units (32768 x 256) 34 and 24. Backward, log form: 240 units (15 x 4096 x
+// 1024) 130 and 132, 128 units 77 and 78, 32 units (65536 x 2048) 300 and 291,
+// 16 units (8192 x 1024) 32 and 26. The tiles of a sequence are
+// equally long: 130 tokens as two of three waves, not of four and one, 95 us
+// against 116 at 240 x 130 x 2048.
 // With many units a tile waits for its predecessor's state alone: it is mostly
-// there, and the folds' words would have to be filled, written and read (2% at
-// 8 x 8192 x 4096). Packed sequences always publish folds: they may be one long
+// there, and the folds' words would have to be filled, written and read (8 x
+// 8192 x 4096: 302 us against 320). Packed sequences always publish folds: they may be one long
 // sequence and many empty ones.
 constexpr int64_t kScanManyUnits = 256;
 // Workgroups that start for n units of one tile: rounded up where they are

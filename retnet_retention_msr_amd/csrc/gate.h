@@ -7,11 +7,13 @@ namespace ret {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// sigmoid(g) and 1 - sigmoid(g), each to a few units in the last place of its
-// own size: with e = exp(-g), a = 1 / (1 + e), and 1 - a = e a where a is the
-// larger of the two, else by subtraction (e overflows there, or its
-// reciprocal is less than the least normal number, which the hardware's makes
-// 0). A NaN stays one in both.
+// sigmoid(g) and 1 - sigmoid(g), each to its own digits: with e = exp(-g), a =
+// 1 / (1 + e), and 1 - a = e a where a is the larger of the two, else by
+// subtraction (e overflows there, or its reciprocal is less than the least
+// normal number, which the hardware's makes 0). The exponent's product is
+// rounded relative to |g|, so that the smaller of the two is off by up to about
+// (|g| + 8) roundings of 2^-24; they add up to 1 but for two. A NaN stays one in
+// both.
 __device__ __forceinline__ void sigmoid_pair(float g, float& a, float& one_less) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * g);
   a = __builtin_amdgcn_rcpf(1.0f + e);

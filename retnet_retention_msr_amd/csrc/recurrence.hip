@@ -37,10 +37,12 @@
 // A gate of -inf (a reset) forgets the state before it whatever it holds, and
 // one of +inf in the sigmoid form passes over whatever x holds, where the
 // formulas' products have 0 times infinity or NaN. A wave in which a lane's A is
-// not above 0, or its Y not finite, takes its tokens a second time, looking at
-// each (`special`); the others are spared that: their tokens have neither. A
-// fold with a reset in it is marked by M = NaN with A = 0; a decay that is 0 in
-// fp32 alone is no reset, and an infinite state stays infinite or becomes NaN.
+// not above 0 (it may hold a reset), or in the sigmoid form a token may have been
+// passed over (forward: a Y that is not finite, backward: a 1 - a of 0), takes
+// its tokens a second time, looking at each (`special`); the others are spared
+// that: without either kind of token the products do what they should. A fold
+// with a reset in it is marked by M = NaN with A = 0; a decay that is 0 in fp32
+// alone is no reset, and an infinite state stays infinite or becomes NaN.
 // Published words hold their own "not there yet" value (all ones, written by
 // scan_fill_kernel before each launch, 1 to 6 us), so one relaxed access is
 // enough.
@@ -129,11 +131,11 @@ __device__ __forceinline__ void mark_resets(uint32_t resets, float (&A)[V], floa
 }
 __device__ __forceinline__ bool resets(float A, float M) { return A == 0.0f && M != M; }
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
-// Whether a lane of the wave has a fold that needs the careful way, or `odd`.
+// Whether a lane of the wave has a fold that may hold a reset, or `odd`.
 template <int V>
-__device__ __forceinline__ bool wave_special(const float (&A)[V], const float (&Y)[V], bool odd) {
+__device__ __forceinline__ bool wave_special(const float (&A)[V], bool odd) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) odd |= !(A[j] > 0.0f) | !finite(Y[j]);
+  for (int j = 0; j < V; ++j) odd |= !(A[j] > 0.0f);
   return __any(odd);
 }
 
@@ -442,7 +444,7 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
       TM = fmaf(g.z, TA, TM);
       TA *= g.x;
     }
-    const bool tile_special = __any(!(TA > 0.0f) | !finite(TY));
+    const bool tile_special = __any(!(TA > 0.0f));
     if (tile_special) {
       TA = 1.0f;
       TY = 0.0f;
@@ -562,10 +564,10 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   // A workgroup whose number stands for a tile past the end takes no ticket: as
   // many are left as the sequence has tiles. An empty sequence's tile 0 passes
   // its state on. With many units the loads start for the tile of the
-  // workgroup's number while the ticket is on its way (backward at 8 x 8192 x
-  // 4096: 600 us against 700); with few, where tickets of neighbouring tiles
-  // cross and such loads are lost, they wait for it (backward of 4 x 7501 x
-  // 1001 fp32: 168 us against 190).
+  // workgroup's number while the ticket is on its way (the backward at 8 x 8192
+  // x 4096 takes a seventh longer without); with few, where tickets of
+  // neighbouring tiles cross and such loads are lost, they wait for it (backward
+  // of 4 x 7501 x 1001 fp32: 167 us against 190).
   if (p.tile > 0 && static_cast<int64_t>(p.tile) * rows >= len) return;
   if (len > 0 && !w.fold) load(p.tile);
   if (tiles > 1) {
@@ -610,7 +612,10 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
     if (careful) mark_resets(zero, A, M);
   };
   fold(std::false_type());
-  const bool special = wave_special(A, Y, false);
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < V; ++j) odd |= FORM == 0 && !finite(Y[j]);
+  const bool special = wave_special(A, odd);
   if (special) {
     load(p.tile);
     fold(std::true_type());
@@ -650,9 +655,9 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // fill: sigmoid form 8 x 8192 x 4096 622 us (5.2 TB/s; 601 without M and the
 // look for special waves), log form 4 x 8192 x 4096 262 us (5.1 TB/s), 65536 x
 // 2048 285 us (4.7 TB/s). Bounds of
-// four waves to a SIMD where the registers suffice: the log form, 252 us
-// against 257; its three tensors of 32 tokens in fp32, or with an fp32 h, do
-// not fit.
+// four waves to a SIMD where the registers suffice, or nearly (the log form in
+// bf16 spills 4 registers): its three tensors of 32 tokens in fp32, or with an
+// fp32 h, do not fit.
 template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
 __global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(TH) == 2 ? 4 : 2)
 recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
@@ -760,13 +765,13 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
     if (careful) mark_resets(zero, A, M);
   };
   fold(std::false_type());
-  const bool special = wave_special(A, Y, FORM == 0 && least == 0.0f);
+  const bool special = wave_special(A, FORM == 0 && least == 0.0f);
   if (special) {
     load(p.tile);
     fold(std::true_type());
   }
   const int64_t unit_state = p.sh * q.d + p.slab * kScanChannels;
-  scan_carry<V, 2>(A, M, Y, y, special, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
+  scan_carry<V, 1>(A, M, Y, y, special, w, p, row0 + rows >= len, grad_state_out ? grad_state_out + unit_state : nullptr,
                 grad_state_in ? grad_state_in + unit_state : nullptr, q.d - p.slab * kScanChannels, at, shared);
   T *dxr = row(grad_x), *dgr = row(grad_gate);
 #pragma unroll
@@ -941,11 +946,11 @@ hipError_t launch_gated_recurrence(int form, int dtype, const View& x, const Vie
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
   // Rows that do not all begin on a cache line: the pieces that two workgroups
-  // write meet within lines and go through the caches (8 x 4096 x 4104 bf16 183
-  // us against 243 past them, 64 x 1024 x 1032 100 against 130, 64 x 640 x 1001
-  // fp32 108 against 125). Where x, gate and h are small enough for the inputs
+  // write meet within lines and go through the caches (8 x 4096 x 4104 bf16 179
+  // us against 239 past them, 64 x 1024 x 1032 98 against 125, 64 x 640 x 1001
+  // fp32 104 against 121). Where x, gate and h are small enough for the inputs
   // to be in the Infinity Cache still, results past it leave them there (176 MB,
-  // 10749 x 2728 bf16: 54 against 46; 240 MB, 2 x 20000 x 1001 bf16: 74 and 75).
+  // 10749 x 2728 bf16: 54 against 46; 240 MB, 2 x 20000 x 1001 bf16: 74 and 76).
   const int64_t size = dtype == 0 ? 4 : 2;
   const int64_t h_size = wide_h ? 4 : size;
   const int64_t rows = int64_t{q.cu ? 1 : q.S} * q.H * q.N;
@@ -989,9 +994,9 @@ hipError_t launch_gated_recurrence_backward(int form, int dtype, const View& gra
   const dim3 grid(static_cast<unsigned>(p.blocks)), block(64 * p.waves);
   // Rows that do not all begin on a cache line: the pieces that two workgroups
   // write meet within lines, and two results of them fare better through the
-  // caches (bf16: 4 x 7501 x 1001 111 us against 131, 55 x 193 x 3824 108
-  // against 132, 10749 x 2728 105 against 108; fp32: 4 x 7501 x 1001 190
-  // against 203, 4 x 19454 x 696 321 against 313).
+  // caches (bf16: 4 x 7501 x 1001 111 us against 128, 55 x 193 x 3824 108
+  // against 130, 10749 x 2728 110 against 113; fp32: 4 x 7501 x 1001 167
+  // against 193, 4 x 19454 x 696 289 against 302).
   const int64_t size = dtype == 0 ? 4 : 2;
   const bool cached = grad_x.sn * size % 128 != 0 || grad_gate.sn * size % 128 != 0;
 #define RET_SCAN(T, TH, FORM, V, E, CACHED)                                                                \

@@ -124,7 +124,7 @@ struct Part {
       }
     }
   }
-  // Adds what is the thread's own to the float row at p.
+  // Puts what is the thread's own into the float row at p.
   __device__ __forceinline__ void put(float* p, const float (&x)[E]) const {
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -386,8 +386,8 @@ gated_norm_backward_kernel(View dy, View o, View gate, View d_o, View d_gate, in
 
 // out[k][head * d + c] = sum over parts of partial[head][part][k][c]: 32
 // columns (a cache line) of a head to a workgroup, 8 threads a column, joined
-// in a fixed order. Grid (columns / 32, sums, heads). 4 us for the 8.4 MB of
-// 1024 parts of 8 heads x 512, 6 us for 25 MB of 512 parts of 4096: the parts
+// in a fixed order. Grid (columns / 32, sums, heads). 4 us for the 4.2 MB of
+// 1024 parts over 8 heads of 512, 6 us for 25 MB of 512 parts of 4096: the parts
 // are mostly in the caches still, the launch and two trips to memory remain.
 __global__ void __launch_bounds__(kThreads)
 param_sum_kernel(const float* partial, int parts, int sums, int d, float* out0, float* out1, float* out2) {
@@ -498,7 +498,7 @@ residual_norm_kernel(View x, View residual, View y, View r, int rows, int N, int
 
 // A thread's running sums, in registers or, where those of a row's three
 // tensors leave no room for them, in LDS of its own (4096 x 16384, whole
-// backward: bf16 171 us against 197, fp32 367 against 525).
+// backward: bf16 159 us against 197, fp32 343 against 525).
 template <int E, bool LDS>
 struct RunningSums {
   float v[E];
@@ -551,8 +551,10 @@ struct RunningSums<E, true> {
 // to 8192 values a row: the case above 235 us with the parameters' sums (5.1
 // TB/s), 8192 x 8192 222 us (5.4 TB/s). Wider rows take 16 values a thread in
 // 1024 threads, two of their three sums in LDS; a CU then has one row at a time
-// and the next one's loads wait for it: 4096 x 16384 bf16 159 us (3.4 TB/s),
-// fp32 343 us (4.7 TB/s).
+// and the next one's loads wait for it, and 17 to 66 of its registers spill:
+// 4096 x 16384 bf16 159 us (3.4 TB/s), fp32 343 us (4.7 TB/s). With a bf16 x and
+// an fp32 stream 2 or 3 spill up to 4096 values a row (8 where the width is
+// ragged).
 template <typename T, typename TR, int L, int V, int K, bool MASK>
 __global__ void __launch_bounds__(threads_of(L), (sizeof(T) == 2 && V * K <= 8) || L == 1024 ? 4 : 2)
 residual_norm_backward_kernel(View dy, View dr, View r, View x, View residual, View dx, View dres, int rows, int N,

@@ -66,7 +66,7 @@ def _strided(t, seed):
 # ---------------------------------------------------------------------------
 # Gated recurrence
 
-# Lengths around the pieces that a sequence is cut into (waves of 16 to 64 tokens, workgroups of up to 512), widths
+# Lengths around the pieces that a sequence is cut into (waves of 8, 16 or 32 tokens, workgroups of up to 256), widths
 # around the 64 channels of a workgroup and the vector widths.
 SHAPES = [
     ((1, 1, 1), "sigmoid", BF16), ((1, 1, 1), "log", F32), ((3, 2, 8), "log", BF16), ((2, 31, 64), "sigmoid", BF16),
