@@ -207,9 +207,11 @@ def _sequences(t, cu_seqlens, max_len):
     return _ints(B, H, N, d), ((S, H, d) if t.dim() == 4 else (S, d)), S, max_len
 
 
-def _h_dtype(t, name, dtype):
-    """The dtype of h, given as a tensor or a dtype (None: the inputs'): the inputs' or float32."""
-    h = dtype if t is None else t if isinstance(t, torch.dtype) else getattr(t, "dtype", dtype)
+def _h_dtype(given, name, dtype):
+    """The dtype of h from a tensor, a dtype or None (the inputs' dtype): the inputs' or float32."""
+    if isinstance(given, torch.Tensor):
+        given = given.dtype
+    h = dtype if given is None else given
     if h not in (dtype, torch.float32):
         raise ValueError(f"{name} must be {dtype} or torch.float32, not {h}")
     return h

@@ -444,3 +444,9 @@ def test_the_residual_stream_may_be_updated_in_place(lib):
     assert call(A[1] + 2) == call(A[1] + 128) == call(A[1], (64, 0, 128)) == call(A[1], y=A[1]) == call(A[0]) == INVALID
     if SHIM:
         assert call(A[1]) == call(A[3]) == 0
+
+
+@pytest.mark.parametrize("bad", ["float32", 3, [torch.zeros(1)], torch.int32])
+def test_what_is_no_dtype_of_h_is_refused(bad):
+    with pytest.raises(ValueError, match="out must be"):
+        block._h_dtype(bad, "out", torch.bfloat16)
