@@ -878,7 +878,9 @@ step_kernel(View x, View gate, View out, int B, int H, int d, float* states, int
         gate_of<FORM>(g[j], a, c);
         if (FORM == 0) v[j] = c == 0.0f ? 0.0f : v[j] * c;
         // As fold_on(): over many steps a's own rounding would add up.
-        now[j] = fold_on(g[j] == -__builtin_inff() ? 0.0f : decay_word(a, -c), v[j], now[j]);
+        const bool near = c <= 0.5f && (FORM == 0 || c >= 0.0f);
+        const float old = g[j] == -__builtin_inff() ? 0.0f : now[j];  // a reset forgets whatever it is
+        now[j] = fmaf(near ? -c : a, old, v[j]) + (near ? old : 0.0f);
       }
       if (in) {
         T* o = row_of<T>(out, i, h) + start;
