@@ -13,8 +13,9 @@
 // takes a tile of tokens of 64 channels, reads it once into registers and
 // writes its outputs once; what the tokens before it contribute reaches it
 // through a few words per tile:
-//   - a lane holds V neighbouring channels (one access, whatever its alignment; where d is no multiple of V the last lane's is moved back to
-//     end with the row) of R = E / V consecutive tokens, and folds them into
+//   - a lane holds V neighbouring channels (one access, whatever its alignment;
+//     where d is no multiple of V the last lane's is moved back to end with the
+//     row) of R = E / V consecutive tokens, and folds them into
 //     (A, Y): y_out = A y_in + Y; pairs of folds join by
 //     (A1, Y1) then (A2, Y2) = (A1 A2, A2 Y1 + Y2). Beside A goes M = A - 1,
 //     formed from the tokens' 1 - a without A's rounding, M = M1 + M2 A1:
@@ -36,13 +37,14 @@
 //     and in fp32, and rounds its outputs once.
 // A gate of -inf (a reset) forgets the state before it whatever it holds, and
 // one of +inf in the sigmoid form passes over whatever x holds, where the
-// formulas' products have 0 times infinity or NaN. A wave in which a lane's A is
-// not above 0 (it may hold a reset), or in the sigmoid form a token may have been
-// passed over (forward: a Y that is not finite, backward: a 1 - a of 0), takes
-// its tokens a second time, looking at each (`special`); the others are spared
-// that: without either kind of token the products do what they should. A fold
-// with a reset in it is marked by M = NaN with A = 0; a decay that is 0 in fp32
-// alone is no reset, and an infinite state stays infinite or becomes NaN.
+// formulas' products have 0 times infinity or NaN. A wave in which a lane may
+// hold a reset (sigmoid form: a decay that is 0, log form: gates whose sum is
+// -inf), or in the sigmoid form a token that is passed over (forward: a Y that is
+// not finite, backward: a 1 - a of 0), takes its tokens a second time, looking at
+// each (`special`); the others are spared that: without either kind of token the
+// products do what they should. A fold with a reset in it is marked by M = NaN
+// with A = 0; a decay that is 0 in fp32 alone is no reset, and an infinite state
+// stays infinite or becomes NaN.
 // Published words hold their own "not there yet" value (all ones, written by
 // scan_fill_kernel before each launch, 1 to 6 us), so one relaxed access is
 // enough.
@@ -108,16 +110,32 @@ __device__ __forceinline__ void lane_decay(int i, float g, float a, float c, flo
     A = i ? A + g : g;
   }
 }
+// Returns whether the lane may hold a reset (in the sigmoid form also where a
+// product of decays above 0 has become 0).
 template <int FORM, int V>
-__device__ __forceinline__ void lane_decays(float (&A)[V], float (&M)[V]) {
+__device__ __forceinline__ bool lane_decays(float (&A)[V], float (&M)[V]) {
+  bool odd = false;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
+    odd |= !(A[j] > (FORM == 0 ? 0.0f : -__builtin_inff()));
     if (FORM == 1) {
       exp_pair(A[j], A[j], M[j]);
       M[j] = -M[j];
     }
     A[j] = M[j] >= -0.5f ? 1.0f + M[j] : A[j];  // one rounding, not one a token
   }
+  return odd;
+}
+// Whether one of a lane's decays is 0 (and not -0, which stands for 1 where it
+// is held as its distance from 1).
+template <int R, int V>
+__device__ __forceinline__ bool any_zero(const float (&a)[R][V]) {
+  bool zero = false;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) zero |= __float_as_uint(a[i][j]) == 0;
+  return zero;
 }
 // Marks the channels whose bit is set in `resets`.
 template <int V>
@@ -131,13 +149,6 @@ __device__ __forceinline__ void mark_resets(uint32_t resets, float (&A)[V], floa
 }
 __device__ __forceinline__ bool resets(float A, float M) { return A == 0.0f && M != M; }
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
-// Whether a lane of the wave has a fold that may hold a reset, or `odd`.
-template <int V>
-__device__ __forceinline__ bool wave_special(const float (&A)[V], bool odd) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) odd |= !(A[j] > 0.0f);
-  return __any(odd);
-}
 
 // The workspace of a launch with more than one tile. A column is a head's slab;
 // the tiles of its sequences have the slots s * tiles + tile, or, packed,
@@ -444,7 +455,7 @@ __device__ __forceinline__ void scan_carry(float (&A)[V], float (&M)[V], float (
       TM = fmaf(g.z, TA, TM);
       TA *= g.x;
     }
-    const bool tile_special = __any(!(TA > 0.0f));
+    const bool tile_special = __any(TM != TM);  // a reset, or a gate that is NaN
     if (tile_special) {
       TA = 1.0f;
       TY = 0.0f;
@@ -581,6 +592,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
   const bool full = row0 + rows <= len;
 
   float a[R][V], b[R][V], A[V], M[V], Y[V], y[V];
+  float lowest = 1.0f;  // of the lane's decays
   auto fold = [&](auto careful) {
     if (!full) {  // tokens past the end: a = 1, x = 0
 #pragma unroll
@@ -600,6 +612,7 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
         const float g = a[i][j];
         float c;
         token_decay<FORM>(g, a[i][j], c);
+        if (FORM == 0) lowest = fminf(lowest, a[i][j]);
         if (FORM == 0) b[i][j] = careful && c == 0.0f ? 0.0f : b[i][j] * c;
         lane_decay<FORM>(i, g, a[i][j], c, A[j], M[j]);
         if (careful) a[i][j] = mark_token(g, a[i][j]);
@@ -608,14 +621,17 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
         Y[j] = i && !reset ? fmaf(a[i][j], Y[j], b[i][j]) : b[i][j];
       }
     }
-    lane_decays<FORM>(A, M);
-    if (careful) mark_resets(zero, A, M);
-  };
-  fold(std::false_type());
-  bool odd = false;
+    bool odd = lane_decays<FORM>(A, M);
+    if (careful) {
+      mark_resets(zero, A, M);
+      return true;
+    }
+    if (FORM == 0) odd = lowest == 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) odd |= FORM == 0 && !finite(Y[j]);
-  const bool special = wave_special(A, odd);
+    for (int j = 0; j < V; ++j) odd |= FORM == 0 && !finite(Y[j]);
+    return odd;
+  };
+  const bool special = __any(fold(std::false_type()));
   if (special) {
     load(p.tile);
     fold(std::true_type());
@@ -761,11 +777,15 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) Y[j] = careful && last[j] == 0.0f ? 0.0f : last[j] * Y[j];
-    lane_decays<FORM>(A, M);
-    if (careful) mark_resets(zero, A, M);
+    bool odd = lane_decays<FORM>(A, M);
+    if (careful) {
+      mark_resets(zero, A, M);
+      return true;
+    }
+    if (FORM == 0 && __any(odd)) odd = any_zero(a);
+    return odd || (FORM == 0 && least == 0.0f);
   };
-  fold(std::false_type());
-  const bool special = wave_special(A, FORM == 0 && least == 0.0f);
+  const bool special = __any(fold(std::false_type()));
   if (special) {
     load(p.tile);
     fold(std::true_type());
