@@ -182,7 +182,8 @@ __device__ __forceinline__ void publish(uint64_t* at, float m, float Y) {
 // infinite.
 __device__ __forceinline__ float decay_word(float A, float M) {
   const float far = A == 0.0f && !resets(A, M) ? __uint_as_float(1u) : A;
-  return M >= -0.5f && M <= 0.0f ? -__builtin_fabsf(M) : far;
+  // A distance that no y has the digits for is none: with an infinite one it would give NaN.
+  return M >= -0.5f && M <= 0.0f ? (M < -0x1p-64f ? M : -0.0f) : far;
 }
 // A y + Y for such a word: near 1 the sum is rounded once, to y's steps.
 __device__ __forceinline__ float fold_on(float m, float Y, float y) {
@@ -668,12 +669,11 @@ recurrence_kernel(View x, View gate, View out, Sequences q, const float* state_i
 // The same from the last token on: token t of the recurrence is row
 // len - 1 - t of the sequence. grad_h and the gate are loaded first; h and x
 // are needed after the carry only and stay in flight until then. bf16, with the
-// fill: sigmoid form 8 x 8192 x 4096 622 us (5.2 TB/s; 601 without M and the
+// fill: sigmoid form 8 x 8192 x 4096 620 us (5.2 TB/s; 601 without M and the
 // look for special waves), log form 4 x 8192 x 4096 262 us (5.1 TB/s), 65536 x
-// 2048 285 us (4.7 TB/s). Bounds of
-// four waves to a SIMD where the registers suffice, or nearly (the log form in
-// bf16 spills 4 registers): its three tensors of 32 tokens in fp32, or with an
-// fp32 h, do not fit.
+// 2048 285 us (4.7 TB/s). Bounds of four waves to a SIMD where the registers
+// suffice, or nearly (the log form in bf16 spills 4): its three tensors of 32
+// tokens in fp32, or with an fp32 h, do not fit.
 template <typename T, typename TH, int FORM, int V, int E, bool CACHED>
 __global__ void __launch_bounds__(64 * kScanMaxWaves, FORM == 0 || sizeof(TH) == 2 ? 4 : 2)
 recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x, View grad_gate, Sequences q,
@@ -750,7 +750,8 @@ recurrence_backward_kernel(View grad_h, View x, View gate, View hv, View grad_x,
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (t0 + i < len) continue;
-        gw[i] = P::all(kKeepGate<FORM>);
+        // Not +inf: a 1 - a of 0 makes the wave special (240 x 317 x 2048 191 us, so 186).
+        gw[i] = P::all(FORM == 0 ? 80.0f : 0.0f);
         dw[i] = P::all(0.0f);
       }
     }

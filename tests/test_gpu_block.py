@@ -1047,6 +1047,22 @@ def test_a_decay_of_one_passes_over_whatever_x_holds():
         assert torch.equal(state, s0) and torch.equal(h, s0)
 
 
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+@pytest.mark.parametrize("B,N,D", [(2, 1, 64), (1, 20, 70), (2, 317, 200), (300, 33, 64)])
+def test_a_sequence_that_is_passed_over_hands_on_what_is_infinite(B, N, D, dtype):
+    """Gates of +inf throughout: the state and its gradient go through as they are, at lengths that fill no tile."""
+    _announce(f"gates of +inf throughout {B} x {N} x {D} {dtype}")
+    x, dh = _randn((B, N, D), 1, dtype).to(DEV), torch.zeros(B, N, D, dtype=dtype, device=DEV)
+    g = torch.full_like(x, float("inf"))
+    s0, ds = _randn((B, D), 2).to(DEV), _randn((B, D), 3).to(DEV)
+    for t in (s0, ds):
+        t[0, ::3], t[-1, 1::3] = float("inf"), -float("inf")
+    h, state = ret.gated_recurrence(x, g, state_in=s0, state_out=True)
+    assert torch.equal(state, s0) and torch.equal(h, s0[:, None].to(dtype).expand(B, N, D))
+    dx, dg, ds0 = ret.gated_recurrence_backward(dh, x, g, h, state_in=s0, grad_state_out=ds, grad_state_in=True)
+    assert torch.equal(ds0, ds) and not bool(dx.any()) and not bool(dg.any())
+
+
 @pytest.mark.parametrize("form", ["sigmoid", "log"])
 def test_a_step_resets_a_slot_of_any_contents(form):
     _announce(f"step resets {form}")
