@@ -43,7 +43,7 @@ constexpr size_t kScanStatusBytes = 256;  // of the workspace: the status word, 
 // Tokens of a wave: forward 32 against 16, bf16, 302 us against 320 at 8 x 8192 x
 // 4096, 157 against 187 at 4 x 8192 x 4096 in the log form. The sigmoid form's
 // backward reads four tensors; waves of 16 tokens let it hold them in 128
-// registers, four waves to a SIMD: 622 us at 8 x 8192 x 4096 against 987 with
+// registers, four waves to a SIMD: 620 us at 8 x 8192 x 4096 against 987 with
 // 32, of which 49 registers spill. 8 where a lane has one channel, so that a
 // short row's tile stays in registers.
 constexpr int kScanRows = 32;
